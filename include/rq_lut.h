@@ -67,7 +67,8 @@ typedef enum rq_status {
   RQ_ERR_HIP = -6         /* a HIP launch failed                               */
 } rq_status;
 
-typedef enum rq_dtype { RQ_F32 = 0, RQ_BF16 = 1 } rq_dtype;
+/* RQ_F16 is a type of the 4-bit matrices, the rotation and the cache; RQ codebooks and tables are fp32 or bf16. */
+typedef enum rq_dtype { RQ_F32 = 0, RQ_BF16 = 1, RQ_F16 = 2 } rq_dtype;
 
 typedef enum rq_prologue {
   RQ_PRO_NONE = 0,          /* the activation is x                                    */
@@ -375,6 +376,167 @@ rq_status rq_dense_logits(const uint16_t* Et, int64_t rows, int32_t D, const flo
  * RQ_ERR_ALIGN.
  */
 rq_status rq_residual_norm(const float* y, float* h, float* x, int32_t D, float eps, hipStream_t stream);
+
+/*
+ * ---- Attention around the RQ-coded parts of a model ----------------------
+ *
+ * The combined variant of the pages keeps attention's projections in 4 bits
+ * beside the RQ-coded embedding (combined RQ+NF4 page). A decoder layer's
+ * attention is four calls: rq_q4_matvec (q, k and v in one stacked matrix),
+ * rq_rope_append, rq_paged_attn, rq_q4_matvec (the output projection).
+ */
+
+/*
+ * A matrix W[rows][D] kept in 4 bits with a scale (and an offset) per group of
+ * columns of a row:
+ *     W[r][k] = scale[r][k / group] * level(code[r][k]) + offset[r][k / group]
+ *   level    code - 8, or levels[code] of a table of 16 bf16 values (finite;
+ *            NF4 and its like)
+ *   rows     0 <= rows < 2^31;  D: 1 <= D <= 65536 (any, odd ones too)
+ *   group    32, 64 or 128 columns; the last group may be short
+ *   scale_dtype   type of scales and offsets: RQ_F32, RQ_BF16 or RQ_F16
+ *   codes    device, the block layout rq_pack_q4_codes writes, 16-byte aligned:
+ *            [ceil(rows/16)][ceil(D/128)] blocks of 1024 bytes; in a block
+ *            [4][16][4] words, word (c, i, w) holding row i's columns
+ *            32w + 8c + j, j < 4 in its nibble 2j, the others in nibble 2j - 7
+ *   scales, offsets  device, the block layout rq_pack_q4_scales writes, 16-byte
+ *            aligned: [ceil(rows/16)][ceil(D/128)][16][128/group]; offsets may be NULL
+ *   levels   device bf16 [16], 4-byte aligned, or NULL
+ * Padding (rows past the last, columns past D) is code 0 and scale 0.
+ */
+typedef struct rq_q4_matrix {
+  int64_t rows;
+  int32_t D, group, scale_dtype;
+  const void* codes;
+  const void* scales;
+  const void* offsets;
+  const uint16_t* levels;
+} rq_q4_matrix;
+
+/* Bytes of the block layout of the codes, and of the scales (0 for invalid arguments). */
+size_t rq_q4_codes_bytes(int64_t rows, int32_t D);
+size_t rq_q4_scales_bytes(int64_t rows, int32_t D, int32_t group, int32_t scale_dtype);
+/*
+ * Convert codes from the interchange layout (src, uint8 [rows][ceil(D/2)], the
+ * even column in the low half of a byte) and scales or offsets from theirs
+ * (src, [rows][ceil(D/group)]) to the block layouts. No overlap.
+ */
+rq_status rq_pack_q4_codes(const uint8_t* src, int64_t rows, int32_t D, void* dst, hipStream_t stream);
+rq_status rq_pack_q4_scales(const void* src, int64_t rows, int32_t D, int32_t group, int32_t scale_dtype, void* dst,
+                            hipStream_t stream);
+
+/*
+ * Product with a 4-bit matrix, for one vector or a batch:
+ *     y[b][r] = sum_k W[r][k] * a[b][k],   a = x, or gelu_tanh(x) * x2 (RQ_PRO_GELU_TANH_MUL)
+ * Products are exact and sums fp32 (fp32 activations enter with all 24 bits).
+ *   x    device [B][D] of x_dtype (RQ_F32, RQ_BF16, RQ_F16), aligned to its type
+ *   x2   device fp32 [B][D], read with the GELU prologue only (x is then fp32)
+ *   B    0 <= B <= 65535;  y device fp32 [B][rows]
+ *   ws   at least rq_q4_matvec_workspace() bytes (0 for few vectors: NULL then)
+ * Deterministic; a vector's result can depend on B in its last bits.
+ */
+size_t rq_q4_matvec_workspace(const rq_q4_matrix* W, int32_t x_dtype, int32_t prologue, int32_t B);
+rq_status rq_q4_matvec(const rq_q4_matrix* W, const void* x, int32_t x_dtype, const float* x2, int32_t prologue, int32_t B,
+                       float* y, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * A paged cache of keys and values. Page p holds page_size tokens of every kv head:
+ *     k [pages][kv_heads][page_size][head_dim]
+ *     v [pages][kv_heads][head_dim][page_size]   (transposed inside a page)
+ *   pages      1 <= pages < 2^31;  page_size 16, 32, 64, 128 or 256
+ *   kv_heads   1..256;  head_dim 2..512, even (rq_paged_attn: 64, 128 or 256)
+ *   dtype      RQ_BF16 or RQ_F16;  k, v 16-byte aligned
+ */
+typedef struct rq_kv_cache {
+  int32_t pages, page_size, kv_heads, head_dim, dtype;
+  void* k;
+  void* v;
+} rq_kv_cache;
+
+/*
+ * The new tokens of a batch of sequences, packed one sequence behind the other,
+ * and where their caches lie. All arrays are device int32.
+ *   seqs, tokens   number of sequences and rows of the packed tensors
+ *   cu_q    [seqs + 1], rising: tokens cu_q[s] .. cu_q[s+1]-1 are sequence s's
+ *           new ones (none is fine; rows from cu_q[seqs] on belong to no one and are
+ *           left as they are)
+ *   lens    [seqs]: tokens of each sequence in the cache, the new ones among
+ *           them as its last: new token i of n lies at place lens[s] - n + i
+ *   table   [seqs][max_pages]: the page of places j*page_size .. of each sequence
+ * Values are not known to the host. A page id outside [0, pages), or a place
+ * beyond the table, is never read or written: its keys are no one's, and the
+ * token is not stored. Pages of different sequences may be shared for reading;
+ * rq_rope_append writes each place that it is given.
+ */
+typedef struct rq_seq_batch {
+  int32_t seqs, tokens, max_pages;
+  const int32_t* cu_q;
+  const int32_t* lens;
+  const int32_t* table;
+} rq_seq_batch;
+
+typedef enum rq_rope_layout {
+  RQ_ROPE_HALF = 0,         /* pairs (i, i + rot/2)  */
+  RQ_ROPE_INTERLEAVED = 1   /* pairs (2i, 2i + 1)    */
+} rq_rope_layout;
+
+/*
+ * Rotary positions. In each head of x, pair i of the first rot values turns:
+ *     (x1, x2) -> mscale * (x1 cos a - x2 sin a, x2 cos a + x1 sin a),  a = position * freqs[i]
+ * and the values from rot on pass unchanged. inverse != 0 turns by -a: the
+ * gradient. Angles are taken in 64 bits. Long-context scaling is in freqs and mscale.
+ *   x, out     device [tokens][heads][head_dim] of x_dtype / out_dtype (any of
+ *              the three types), heads contiguous, x_stride / out_stride elements
+ *              (>= heads*head_dim) from token to token, aligned to their types; out may be x itself (same
+ *              type and stride) but must not overlap it otherwise
+ *   heads 1..4096; head_dim 2..512, even; rot 2..head_dim, even
+ *   positions  device int32 [tokens];  freqs device double [rot/2], 8-byte aligned
+ */
+rq_status rq_rope(const void* x, int32_t x_dtype, int32_t tokens, int32_t heads, int32_t head_dim, int64_t x_stride,
+                  const int32_t* positions, const double* freqs, int32_t rot, int32_t layout, float mscale, int32_t inverse,
+                  void* out, int32_t out_dtype, int64_t out_stride, hipStream_t stream);
+
+/*
+ * One step's queries, keys and values: q is rotated into q_out, k is rotated
+ * into the cache, v goes into the cache; all are rounded once to its type.
+ *   q          device [tokens][heads][head_dim] of in_dtype; heads a multiple of kv_heads
+ *   k, v       device [tokens][kv_heads][head_dim] of in_dtype; token strides in
+ *              elements as for rq_rope (views of one stacked projection are fine)
+ *   positions  device int32 [tokens], or NULL: each token's place in its cache
+ *   q_out      device [tokens][heads][head_dim] of the cache's type, contiguous, overlapping no input
+ *   bad_pages  device int32 counter or NULL (not reset): raised by the number of
+ *              tokens whose place has no page
+ * Two tokens given the same place (a page in two tables) race.
+ */
+rq_status rq_rope_append(const rq_seq_batch* batch, const rq_kv_cache* cache, const void* q, const void* k, const void* v,
+                         int32_t in_dtype, int64_t q_stride, int64_t k_stride, int64_t v_stride, int32_t heads,
+                         const int32_t* positions, const double* freqs, int32_t rot, int32_t layout, float mscale,
+                         void* q_out, int32_t* bad_pages, hipStream_t stream);
+
+/*
+ * Attention of each sequence's new tokens over its cache: single tokens,
+ * drafts, chunks behind a context and whole prompts alike.
+ *     z_j = scale * <q, k_j>   (softcap > 0: softcap * tanh(z_j / softcap))
+ *     out = sum_j softmax(z)_j v_j  over the places j <= place of the token,
+ *                                   and j > place - window where window > 0
+ * Query head h reads kv head h / (heads / kv_heads). A token that sees no key
+ * gives zeros and lse = -inf. What lies in unseen places (stale pages, the rest
+ * of a page, later tokens of the chunk) has no influence, infinities and NaN included.
+ *   q        device [tokens][heads][head_dim] of the cache's type, q_stride
+ *            elements from token to token (a multiple of 8), 16-byte aligned
+ *   max_len  an upper bound of lens (it sizes the workspace and the split of
+ *            the keys; results stay right if it is exceeded); 0: none known
+ *   out      device [tokens][heads][head_dim], contiguous, 16-byte aligned; not overlapping q
+ *   lse      device fp32 [tokens][heads]: log of the sum of exp(z_j), or NULL
+ *   bad_pages  device int32 counter or NULL (not reset): raised by the number of
+ *            used table entries that name no page (one more launch)
+ *   ws       at least rq_paged_attn_workspace() bytes of the same sizes
+ * Scores, maxima, sums and outputs are held in fp32. Deterministic.
+ */
+size_t rq_paged_attn_workspace(const rq_kv_cache* cache, int32_t tokens, int32_t seqs, int32_t heads, int32_t max_len);
+rq_status rq_paged_attn(const rq_seq_batch* batch, const rq_kv_cache* cache, const void* q, int64_t q_stride, int32_t heads,
+                        float scale, float softcap, int32_t window, int32_t max_len, void* out, float* lse,
+                        int32_t* bad_pages, void* ws, size_t ws_bytes, hipStream_t stream);
 
 /* Static text for a status code. Takes any int (an rq_status value converts
  * to it); a value that is no rq_status gives "unknown status". */

@@ -16,12 +16,13 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("RQ_LUT_LIB") or os.path.join(HERE, "librq_lut.so")
 
 RQ_OK, RQ_ERR_NULL, RQ_ERR_SHAPE, RQ_ERR_DTYPE, RQ_ERR_ALIGN, RQ_ERR_WORKSPACE, RQ_ERR_HIP = 0, -1, -2, -3, -4, -5, -6
-RQ_F32, RQ_BF16 = 0, 1
+RQ_F32, RQ_BF16, RQ_F16 = 0, 1, 2
 RQ_PRO_NONE, RQ_PRO_GELU_TANH_MUL = 0, 1
 RQ_CODES_ROWS, RQ_CODES_BLOCKED, RQ_CODES_PACKED10, RQ_CODES_PACKED8 = 0, 1, 2, 3
 _LAYOUTS = {"rows": RQ_CODES_ROWS, "blocked": RQ_CODES_BLOCKED, "packed10": RQ_CODES_PACKED10,
             "packed8": RQ_CODES_PACKED8}
 RQ_METHOD_TABLE, RQ_METHOD_MATRIX_CORES = 0, 1
+RQ_ROPE_HALF, RQ_ROPE_INTERLEAVED = 0, 1
 
 # Every symbol include/rq_lut.h declares.
 EXPORTS = ("rq_blocked_codes_bytes", "rq_pack_codes", "rq_packed10_codes_bytes", "rq_pack_codes10",
@@ -30,7 +31,9 @@ EXPORTS = ("rq_blocked_codes_bytes", "rq_pack_codes", "rq_packed10_codes_bytes",
            "rq_lut_mlp_workspace", "rq_lut_mlp", "rq_residual_norm", "rq_dense_tiled_bytes", "rq_pack_dense", "rq_dense_logits_workspace", "rq_dense_logits", "rq_stream_read_configs",
            "rq_stream_read_sink_words", "rq_stream_read", "rq_lds_gather_sink_words", "rq_lds_gather",
            "rq_set_stage_events", "rq_lut_logits_plan", "rq_status_string",
-           "rq_last_error", "rq_version")
+           "rq_last_error", "rq_version", "rq_q4_codes_bytes", "rq_q4_scales_bytes", "rq_pack_q4_codes",
+           "rq_pack_q4_scales", "rq_q4_matvec_workspace", "rq_q4_matvec", "rq_rope", "rq_rope_append",
+           "rq_paged_attn_workspace", "rq_paged_attn")
 
 
 class RQError(RuntimeError):
@@ -45,9 +48,26 @@ class rq_matrix(ctypes.Structure):
                 ("codes_layout", ctypes.c_int32), ("codebooks", ctypes.c_void_p), ("codes", ctypes.c_void_p)]
 
 
+class rq_q4_matrix(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("D", ctypes.c_int32), ("group", ctypes.c_int32),
+                ("scale_dtype", ctypes.c_int32), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("offsets", ctypes.c_void_p), ("levels", ctypes.c_void_p)]
+
+
+class rq_kv_cache(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p)]
+
+
+class rq_seq_batch(ctypes.Structure):
+    _fields_ = [("seqs", ctypes.c_int32), ("tokens", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("cu_q", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("table", ctypes.c_void_p)]
+
+
 _lib = None
 _i32, _i64, _sz, _vp, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_float
 _MP = ctypes.POINTER(rq_matrix)
+_QP, _CP, _BP = ctypes.POINTER(rq_q4_matrix), ctypes.POINTER(rq_kv_cache), ctypes.POINTER(rq_seq_batch)
 
 
 def lib():
@@ -92,6 +112,17 @@ def lib():
             "rq_status_string": (ctypes.c_char_p, [_i32]),
             "rq_last_error": (ctypes.c_char_p, []),
             "rq_version": (ctypes.c_char_p, []),
+            "rq_q4_codes_bytes": (_sz, [_i64, _i32]),
+            "rq_q4_scales_bytes": (_sz, [_i64, _i32, _i32, _i32]),
+            "rq_pack_q4_codes": (_i32, [_vp, _i64, _i32, _vp, _vp]),
+            "rq_pack_q4_scales": (_i32, [_vp, _i64, _i32, _i32, _i32, _vp, _vp]),
+            "rq_q4_matvec_workspace": (_sz, [_QP, _i32, _i32, _i32]),
+            "rq_q4_matvec": (_i32, [_QP, _vp, _i32, _vp, _i32, _i32, _vp, _vp, _sz, _vp]),
+            "rq_rope": (_i32, [_vp, _i32, _i32, _i32, _i32, _i64, _vp, _vp, _i32, _i32, _f32, _i32, _vp, _i32, _i64, _vp]),
+            "rq_rope_append": (_i32, [_BP, _CP, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _i32, _vp, _vp, _i32, _i32, _f32,
+                                      _vp, _vp, _vp]),
+            "rq_paged_attn_workspace": (_sz, [_CP, _i32, _i32, _i32, _i32]),
+            "rq_paged_attn": (_i32, [_BP, _CP, _vp, _i64, _i32, _f32, _f32, _i32, _i32, _vp, _vp, _vp, _vp, _sz, _vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -495,3 +526,257 @@ def set_stage_events(before, after):
             ev.record()
         return ctypes.c_void_p(ev.cuda_event)
     check(lib().rq_set_stage_events(handle(before), handle(after)))
+
+
+# ---- attention around the RQ-coded parts: 4-bit projections, rotation and cache, attention
+
+_TYPES = {torch.float32: RQ_F32, torch.bfloat16: RQ_BF16, torch.float16: RQ_F16}
+
+
+def _one_device(**tensors):
+    """Every tensor of a call must live on one GPU. Returns its index."""
+    _gpu(**tensors)
+    first = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if first is None:
+            first = t.device.index
+        elif t.device.index != first:
+            raise ValueError(f"{name}: on {t.device}, the other tensors are on cuda:{first}")
+    return first
+
+
+def _call(fn, dev, *args):
+    """fn(*args, stream) on device dev's current stream, with that device current for the launch."""
+    if torch.cuda.current_device() == dev:
+        check(fn(*args, _stream()))
+    else:
+        with torch.cuda.device(dev):
+            check(fn(*args, _stream()))
+
+
+def _typed(t, name, types=tuple(_TYPES)):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.dtype not in types:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected one of {', '.join(str(x) for x in types)}")
+    return t
+
+
+def _heads_arg(t, name, heads=None, size=None, tokens=None, dtype=None):
+    """A [tokens][heads][size] tensor whose heads lie one behind the other; tokens may be further apart (a
+    view of a stacked projection). Returns the token stride in elements."""
+    _typed(t, name, tuple(_TYPES) if dtype is None else (dtype,))
+    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or (size is not None and t.shape[2] != size) or \
+            (tokens is not None and t.shape[0] != tokens):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected "
+                         f"({'tokens' if tokens is None else tokens}, {heads or 'heads'}, {size or 'size'})")
+    if (t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{name}: the heads of a token must be contiguous (strides {t.stride()})")
+    width = t.shape[1] * t.shape[2]
+    stride = t.stride(0) if t.shape[0] > 1 else width
+    if stride < width:
+        raise ValueError(f"{name}: tokens overlap (strides {t.stride()})")
+    return stride
+
+
+def _scratch(ws, need, dev):
+    """The caller's workspace, checked, or a new one (None where none is needed)."""
+    if ws is not None:
+        return _arg(ws, "ws", torch.uint8, min_numel=need)
+    return torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+
+
+class Q4Matrix:
+    """A matrix [rows][D] in 4 bits with scales (and offsets) per group of columns, in the library's block layout
+    (rq_q4_matrix in include/rq_lut.h; made by pack_q4, or from tensors that already hold the layout).
+
+    codes: uint8, q4_codes_bytes(rows, D) of them; scales, offsets: float32, bfloat16 or float16; levels: 16 bfloat16
+    values, or None (code - 8)."""
+
+    def __init__(self, rows, D, group, codes, scales, offsets=None, levels=None):
+        _typed(scales, "scales")
+        nb = lib().rq_q4_scales_bytes(rows, D, group, _TYPES[scales.dtype])
+        if rows and not nb:
+            raise RQError(RQ_ERR_SHAPE, f"4-bit matrix {rows} x {D} with groups of {group} out of range")
+        _arg(codes, "codes", torch.uint8, numel=q4_codes_bytes(rows, D))
+        _arg(scales, "scales", scales.dtype, numel=nb // scales.element_size())
+        if offsets is not None:
+            _arg(offsets, "offsets", scales.dtype, numel=scales.numel())
+        if levels is not None:
+            _arg(levels, "levels", torch.bfloat16, numel=16)
+        self.rows, self.D, self.group = rows, D, group
+        self.codes, self.scales, self.offsets, self.levels = codes, scales, offsets, levels
+        self.desc = rq_q4_matrix(rows, D, group, _TYPES[scales.dtype], *(t.data_ptr() if t is not None else None
+                                                                         for t in (codes, scales, offsets, levels)))
+
+    @property
+    def ref(self):
+        return ctypes.byref(self.desc)
+
+    def resident_bytes(self):
+        return sum(t.numel() * t.element_size() for t in (self.codes, self.scales, self.offsets, self.levels) if t is not None)
+
+
+def q4_codes_bytes(rows, D):
+    return lib().rq_q4_codes_bytes(rows, D)
+
+
+def pack_q4(codes, scales, D, group, offsets=None, levels=None):
+    """rq_pack_q4_codes and rq_pack_q4_scales: a Q4Matrix from the interchange layout (codes uint8
+    [rows][ceil(D/2)], even columns in the low halves; scales and offsets [rows][ceil(D/group)])."""
+    if codes.dim() != 2:
+        raise ValueError("codes: expected [rows][ceil(D/2)]")
+    rows, groups = codes.shape[0], -(-D // group) if group else 0
+    _arg(codes, "codes", torch.uint8, shape=(rows, (D + 1) // 2))
+    _typed(scales, "scales")
+    st = _TYPES[scales.dtype]
+    nb = lib().rq_q4_scales_bytes(rows, D, group, st)
+    if rows and not nb:
+        raise RQError(RQ_ERR_SHAPE, f"4-bit matrix {rows} x {D} with groups of {group} out of range")
+    for name, t in (("scales", scales), ("offsets", offsets)):
+        if t is not None:
+            _arg(t, name, scales.dtype, shape=(rows, groups))
+    dev = _one_device(codes=codes, scales=scales, offsets=offsets, levels=levels)
+    packed = torch.empty(q4_codes_bytes(rows, D), dtype=torch.uint8, device=codes.device)
+    _call(lib().rq_pack_q4_codes, dev, _ptr(codes), rows, D, _ptr(packed))
+    blocks = []
+    for t in (scales, offsets):
+        if t is None:
+            blocks.append(None)
+            continue
+        blocks.append(torch.empty(nb // t.element_size(), dtype=t.dtype, device=t.device))
+        _call(lib().rq_pack_q4_scales, dev, _ptr(t), rows, D, group, st, _ptr(blocks[-1]))
+    return Q4Matrix(rows, D, group, packed, *blocks, levels)
+
+
+def q4_matvec_workspace(W, B, x_dtype=torch.float32, prologue=RQ_PRO_NONE):
+    return lib().rq_q4_matvec_workspace(W.ref, _TYPES[x_dtype], prologue, B)
+
+
+def q4_matvec(W, x, x2=None, prologue=RQ_PRO_NONE, ws=None, out=None):
+    """rq_q4_matvec: y [B][rows] fp32 = W a for a Q4Matrix, a = x (float32, bfloat16 or float16) or gelu_tanh(x) * x2."""
+    if not isinstance(W, Q4Matrix):
+        raise TypeError("q4_matvec takes a Q4Matrix")
+    _typed(x, "x")
+    B = x.shape[0] if x.dim() == 2 else -1
+    _arg(x, "x", x.dtype, shape=(B, W.D))
+    if x2 is not None:
+        _arg(x2, "x2", torch.float32, shape=(B, W.D))
+    y = out if out is not None else torch.empty((B, W.rows), dtype=torch.float32, device=x.device)
+    _arg(y, "out", torch.float32, numel=B * W.rows)
+    ws = _scratch(ws, q4_matvec_workspace(W, B, x.dtype, prologue), x.device)
+    dev = _one_device(x=x, x2=x2, out=y, ws=ws, codes=W.codes, scales=W.scales, offsets=W.offsets, levels=W.levels)
+    _call(lib().rq_q4_matvec, dev, W.ref, _ptr(x), _TYPES[x.dtype], _ptr(x2), prologue, B, _ptr(y), _ptr(ws),
+          ws.numel() if ws is not None else 0)
+    return y
+
+
+class KVCache:
+    """A paged cache: k [pages][kv_heads][page_size][head_dim], v [pages][kv_heads][head_dim][page_size], both bfloat16 or
+    float16 (rq_kv_cache)."""
+
+    def __init__(self, k, v):
+        _typed(k, "k", (torch.bfloat16, torch.float16))
+        if k.dim() != 4:
+            raise ValueError("k: expected [pages][kv_heads][page_size][head_dim]")
+        pages, kv_heads, page_size, head_dim = k.shape
+        _arg(k, "k", k.dtype)
+        _arg(v, "v", k.dtype, shape=(pages, kv_heads, head_dim, page_size))
+        self.pages, self.kv_heads, self.page_size, self.head_dim = pages, kv_heads, page_size, head_dim
+        self.k, self.v, self.dtype = k, v, k.dtype
+        self.desc = rq_kv_cache(pages, page_size, kv_heads, head_dim, _TYPES[k.dtype], k.data_ptr(), v.data_ptr())
+
+    @classmethod
+    def empty(cls, pages, kv_heads, page_size, head_dim, dtype=torch.bfloat16, device="cuda"):
+        """A cache with nothing in it (its memory is not cleared: unseen places have no influence)."""
+        return cls(torch.empty((pages, kv_heads, page_size, head_dim), dtype=dtype, device=device),
+                   torch.empty((pages, kv_heads, head_dim, page_size), dtype=dtype, device=device))
+
+    @property
+    def ref(self):
+        return ctypes.byref(self.desc)
+
+
+def _batch(tokens, cu_q, lens, table):
+    """The rq_seq_batch of int32 tensors cu_q [seqs + 1], lens [seqs], table [seqs][max_pages]."""
+    seqs = lens.shape[0] if isinstance(lens, torch.Tensor) and lens.dim() == 1 else -1
+    _arg(lens, "lens", torch.int32, shape=(seqs,))
+    _arg(cu_q, "cu_q", torch.int32, shape=(seqs + 1,))
+    max_pages = table.shape[1] if isinstance(table, torch.Tensor) and table.dim() == 2 else -1
+    _arg(table, "table", torch.int32, shape=(seqs, max_pages))
+    return rq_seq_batch(seqs, tokens, max_pages, cu_q.data_ptr(), lens.data_ptr(), table.data_ptr())
+
+
+_ROPE_LAYOUTS = {"half": RQ_ROPE_HALF, "interleaved": RQ_ROPE_INTERLEAVED}
+
+
+def rope(x, positions, freqs, layout="half", mscale=1.0, inverse=False, out=None, out_dtype=None):
+    """rq_rope: x [tokens][heads][size] with the first 2 * len(freqs) values of each head turned by
+    positions[t] * freqs[i] (freqs float64, see rope_freqs); inverse=True turns back (the gradient). x's tokens may be
+    strided. out (contiguous heads, x's own memory allowed) or a new tensor of out_dtype (x's by default)."""
+    xs = _heads_arg(x, "x")
+    T, heads, size = x.shape
+    _arg(positions, "positions", torch.int32, shape=(T,))
+    _arg(freqs, "freqs", torch.float64, shape=(freqs.numel(),))
+    if out is None:
+        out = torch.empty((T, heads, size), dtype=out_dtype or x.dtype, device=x.device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError(f"out: dtype {out.dtype}, expected {out_dtype}")
+    os_ = _heads_arg(out, "out", heads, size, T)
+    dev = _one_device(x=x, positions=positions, freqs=freqs, out=out)
+    _call(lib().rq_rope, dev, _ptr(x), _TYPES[x.dtype], T, heads, size, xs, _ptr(positions), _ptr(freqs), 2 * freqs.numel(),
+          _ROPE_LAYOUTS[layout], mscale, int(inverse), _ptr(out), _TYPES[out.dtype], os_)
+    return out
+
+
+def rope_append(q, k, v, cache, cu_q, lens, table, freqs, layout="half", mscale=1.0, positions=None, out=None, bad_pages=None):
+    """rq_rope_append: q rotated (returned, in the cache's type), k rotated and v stored in the KVCache at the places of the
+    sequences' newest tokens. q [tokens][heads][size], k and v [tokens][kv_heads][size], of one type, tokens may be strided."""
+    qs = _heads_arg(q, "q", size=cache.head_dim)
+    T, heads = q.shape[:2]
+    ks = _heads_arg(k, "k", cache.kv_heads, cache.head_dim, T, q.dtype)
+    vs = _heads_arg(v, "v", cache.kv_heads, cache.head_dim, T, q.dtype)
+    batch = _batch(T, cu_q, lens, table)
+    _arg(freqs, "freqs", torch.float64, shape=(freqs.numel(),))
+    if positions is not None:
+        _arg(positions, "positions", torch.int32, shape=(T,))
+    if bad_pages is not None:
+        _arg(bad_pages, "bad_pages", torch.int32, min_numel=1)
+    if out is None:
+        out = torch.empty((T, heads, cache.head_dim), dtype=cache.dtype, device=q.device)
+    _arg(out, "out", cache.dtype, shape=(T, heads, cache.head_dim))
+    dev = _one_device(q=q, k=k, v=v, out=out, cache=cache.k, cache_v=cache.v, cu_q=cu_q, lens=lens, table=table, freqs=freqs,
+                      positions=positions, bad_pages=bad_pages)
+    _call(lib().rq_rope_append, dev, ctypes.byref(batch), cache.ref, _ptr(q), _ptr(k), _ptr(v), _TYPES[q.dtype], qs, ks, vs, heads,
+          _ptr(positions), _ptr(freqs), 2 * freqs.numel(), _ROPE_LAYOUTS[layout], mscale, _ptr(out), _ptr(bad_pages))
+    return out
+
+
+def paged_attn_workspace(cache, tokens, seqs, heads, max_len=0):
+    return lib().rq_paged_attn_workspace(cache.ref, tokens, seqs, heads, max_len)
+
+
+def paged_attn(q, cache, cu_q, lens, table, scale=None, softcap=0.0, window=0, max_len=0, ws=None, out=None, lse=None,
+               bad_pages=None):
+    """rq_paged_attn: attention of each sequence's newest tokens over its cache, [tokens][heads][size] of the cache's type.
+    q [tokens][heads][size] (tokens may be strided); scale defaults to size ** -0.5; max_len: an upper bound of lens if one
+    is known; lse: a float32 [tokens][heads] tensor to fill."""
+    qs = _heads_arg(q, "q", size=cache.head_dim, dtype=cache.dtype)
+    T, heads = q.shape[:2]
+    batch = _batch(T, cu_q, lens, table)
+    if out is None:
+        out = torch.empty((T, heads, cache.head_dim), dtype=cache.dtype, device=q.device)
+    _arg(out, "out", cache.dtype, shape=(T, heads, cache.head_dim))
+    if lse is not None:
+        _arg(lse, "lse", torch.float32, shape=(T, heads))
+    if bad_pages is not None:
+        _arg(bad_pages, "bad_pages", torch.int32, min_numel=1)
+    ws = _scratch(ws, paged_attn_workspace(cache, T, batch.seqs, heads, max_len), q.device)
+    dev = _one_device(q=q, out=out, cache=cache.k, cache_v=cache.v, cu_q=cu_q, lens=lens, table=table, lse=lse,
+                      bad_pages=bad_pages, ws=ws)
+    _call(lib().rq_paged_attn, dev, ctypes.byref(batch), cache.ref, _ptr(q), qs, heads,
+          cache.head_dim ** -0.5 if scale is None else scale, softcap, window, max_len, _ptr(out), _ptr(lse), _ptr(bad_pages),
+          _ptr(ws), ws.numel() if ws is not None else 0)
+    return out

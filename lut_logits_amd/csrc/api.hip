@@ -650,6 +650,264 @@ rq_status rq_lut_logits_plan(const rq_matrix* W, int32_t B, int32_t lut_dtype, i
 
 }  // extern "C"
 
+// ---- attention around the RQ-coded parts: 4-bit projections, rotation and cache, attention
+
+namespace {
+
+bool any_dtype(int32_t t) { return t == RQ_F32 || t == RQ_BF16 || t == RQ_F16; }
+size_t dtype_bytes(int32_t t) { return t == RQ_F32 ? 4 : 2; }
+
+rq_status check_q4_shape(int64_t rows, int32_t D) {
+  if (rows < 0 || rows >= ((int64_t)1 << 31)) return fail(RQ_ERR_SHAPE, "rows=%lld out of range", (long long)rows);
+  if (D < 1 || D > 65536) return fail(RQ_ERR_SHAPE, "D=%d outside [1, 65536]", D);
+  return RQ_OK;
+}
+
+rq_status check_q4_groups(int32_t group, int32_t scale_dtype) {
+  if (group != 32 && group != 64 && group != 128) return fail(RQ_ERR_SHAPE, "group=%d is not 32, 64 or 128", group);
+  if (!any_dtype(scale_dtype)) return fail(RQ_ERR_DTYPE, "unknown scale dtype %d", scale_dtype);
+  return RQ_OK;
+}
+
+rq_status check_q4(const rq_q4_matrix* W) {
+  if (!W) return fail(RQ_ERR_NULL, "4-bit matrix descriptor is NULL");
+  rq_status s = check_q4_shape(W->rows, W->D);
+  return s != RQ_OK ? s : check_q4_groups(W->group, W->scale_dtype);
+}
+
+// What rq_q4_matvec and its workspace query ask of types and sizes.
+rq_status check_q4_call(const rq_q4_matrix* W, int32_t x_dtype, int32_t prologue, int32_t B) {
+  rq_status s = check_q4(W);
+  if (s != RQ_OK) return s;
+  if (!any_dtype(x_dtype)) return fail(RQ_ERR_DTYPE, "unknown activation dtype %d", x_dtype);
+  if (prologue != RQ_PRO_NONE && prologue != RQ_PRO_GELU_TANH_MUL)
+    return fail(RQ_ERR_DTYPE, "unknown prologue %d", prologue);
+  if (prologue == RQ_PRO_GELU_TANH_MUL && x_dtype != RQ_F32)
+    return fail(RQ_ERR_DTYPE, "the GELU prologue takes fp32 activations");
+  if (B < 0 || B > 65535) return fail(RQ_ERR_SHAPE, "B=%d outside [0, 65535]", B);
+  return RQ_OK;
+}
+
+rq_status check_heads(int32_t heads, int32_t head_dim) {
+  if (heads < 1 || heads > 4096) return fail(RQ_ERR_SHAPE, "heads=%d outside [1, 4096]", heads);
+  if (head_dim < 2 || head_dim > 512 || head_dim % 2) return fail(RQ_ERR_SHAPE, "head_dim=%d is not even in [2, 512]", head_dim);
+  return RQ_OK;
+}
+
+rq_status check_tokens(int32_t tokens, int32_t heads) {
+  if (tokens < 0 || (int64_t)tokens * heads >= ((int64_t)1 << 31))
+    return fail(RQ_ERR_SHAPE, "tokens=%d with %d heads out of range", tokens, heads);
+  return RQ_OK;
+}
+
+rq_status check_rotation(int32_t rot, int32_t head_dim, int32_t layout, const double* freqs, const int32_t* positions) {
+  if (rot < 2 || rot > head_dim || rot % 2) return fail(RQ_ERR_SHAPE, "rot=%d is not even in [2, head_dim=%d]", rot, head_dim);
+  if (layout != RQ_ROPE_HALF && layout != RQ_ROPE_INTERLEAVED) return fail(RQ_ERR_DTYPE, "unknown rotation layout %d", layout);
+  if (!freqs) return fail(RQ_ERR_NULL, "freqs is NULL");
+  if (!aligned(freqs, 8) || !aligned(positions, 4)) return fail(RQ_ERR_ALIGN, "freqs or positions misaligned");
+  return RQ_OK;
+}
+
+rq_status check_stride(const char* what, int64_t stride, int32_t heads, int32_t head_dim) {
+  if (stride < (int64_t)heads * head_dim || stride > ((int64_t)1 << 31))
+    return fail(RQ_ERR_SHAPE, "%s: token stride %lld below %d x %d or above 2^31", what, (long long)stride, heads, head_dim);
+  return RQ_OK;
+}
+
+rq_status check_cache_shape(const rq_kv_cache* c) {
+  if (!c) return fail(RQ_ERR_NULL, "cache descriptor is NULL");
+  if (c->pages < 1) return fail(RQ_ERR_SHAPE, "pages=%d < 1", c->pages);
+  if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1)))
+    return fail(RQ_ERR_SHAPE, "page_size=%d is not 16, 32, 64, 128 or 256", c->page_size);
+  if (c->kv_heads < 1 || c->kv_heads > 256) return fail(RQ_ERR_SHAPE, "kv_heads=%d outside [1, 256]", c->kv_heads);
+  if (c->head_dim < 2 || c->head_dim > 512 || c->head_dim % 2)
+    return fail(RQ_ERR_SHAPE, "head_dim=%d is not even in [2, 512]", c->head_dim);
+  if (c->dtype != RQ_BF16 && c->dtype != RQ_F16) return fail(RQ_ERR_DTYPE, "cache dtype %d is not bf16 or fp16", c->dtype);
+  return RQ_OK;
+}
+
+rq_status check_cache(const rq_kv_cache* c) {
+  rq_status s = check_cache_shape(c);
+  if (s != RQ_OK) return s;
+  if (!c->k || !c->v) return fail(RQ_ERR_NULL, "cache: k or v is NULL");
+  if (!aligned(c->k, 16) || !aligned(c->v, 16)) return fail(RQ_ERR_ALIGN, "cache: k and v must be 16-byte aligned");
+  return RQ_OK;
+}
+
+rq_status check_batch(const rq_seq_batch* b, int32_t heads) {
+  if (!b) return fail(RQ_ERR_NULL, "batch descriptor is NULL");
+  if (b->seqs < 0 || b->seqs > (1 << 24)) return fail(RQ_ERR_SHAPE, "seqs=%d out of range", b->seqs);
+  rq_status s = check_tokens(b->tokens, heads);
+  if (s != RQ_OK) return s;
+  if (b->max_pages < 0) return fail(RQ_ERR_SHAPE, "max_pages=%d < 0", b->max_pages);
+  if (b->seqs == 0 || b->tokens == 0) return RQ_OK;
+  if (!b->cu_q || !b->lens || (!b->table && b->max_pages > 0)) return fail(RQ_ERR_NULL, "batch: cu_q, lens or table is NULL");
+  if (!aligned(b->cu_q, 4) || !aligned(b->lens, 4) || !aligned(b->table, 4))
+    return fail(RQ_ERR_ALIGN, "batch: cu_q, lens or table misaligned");
+  return RQ_OK;
+}
+
+// What rq_paged_attn and its workspace query ask of types and sizes.
+rq_status check_attn_call(const rq_kv_cache* c, int32_t tokens, int32_t seqs, int32_t heads, int32_t max_len) {
+  rq_status s = check_cache_shape(c);
+  if (s != RQ_OK) return s;
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256)
+    return fail(RQ_ERR_SHAPE, "attention takes head_dim 64, 128 or 256 (got %d)", c->head_dim);
+  s = check_heads(heads, c->head_dim);
+  if (s != RQ_OK) return s;
+  if (heads % c->kv_heads) return fail(RQ_ERR_SHAPE, "heads=%d is no multiple of kv_heads=%d", heads, c->kv_heads);
+  s = check_tokens(tokens, heads);
+  if (s != RQ_OK) return s;
+  if (seqs < 0 || ((int64_t)tokens * heads / c->kv_heads + seqs) * c->kv_heads >= ((int64_t)1 << 31))
+    return fail(RQ_ERR_SHAPE, "seqs=%d out of range", seqs);
+  if (max_len < 0) return fail(RQ_ERR_SHAPE, "max_len=%d < 0", max_len);
+  return RQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t rq_q4_codes_bytes(int64_t rows, int32_t D) {
+  return check_q4_shape(rows, D) == RQ_OK ? rq::q4_codes_bytes(rows, D) : 0;
+}
+
+size_t rq_q4_scales_bytes(int64_t rows, int32_t D, int32_t group, int32_t scale_dtype) {
+  if (check_q4_shape(rows, D) != RQ_OK || check_q4_groups(group, scale_dtype) != RQ_OK) return 0;
+  return rq::q4_scale_count(rows, D, group) * dtype_bytes(scale_dtype);
+}
+
+rq_status rq_pack_q4_codes(const uint8_t* src, int64_t rows, int32_t D, void* dst, hipStream_t stream) {
+  CallRange range(__func__);
+  rq_status s = check_q4_shape(rows, D);
+  if (s != RQ_OK || rows == 0) return s;
+  if (!src || !dst) return fail(RQ_ERR_NULL, "pack_q4_codes: NULL buffer");
+  if (!aligned(dst, 16)) return fail(RQ_ERR_ALIGN, "pack_q4_codes: dst must be 16-byte aligned");
+  return launched(rq::launch_pack_q4_codes(src, rows, D, dst, stream), "rq_pack_q4_codes");
+}
+
+rq_status rq_pack_q4_scales(const void* src, int64_t rows, int32_t D, int32_t group, int32_t scale_dtype, void* dst,
+                            hipStream_t stream) {
+  CallRange range(__func__);
+  rq_status s = check_q4_shape(rows, D);
+  if (s == RQ_OK) s = check_q4_groups(group, scale_dtype);
+  if (s != RQ_OK || rows == 0) return s;
+  if (!src || !dst) return fail(RQ_ERR_NULL, "pack_q4_scales: NULL buffer");
+  const size_t eb = dtype_bytes(scale_dtype);
+  if (!aligned(src, eb) || !aligned(dst, 16)) return fail(RQ_ERR_ALIGN, "pack_q4_scales: misaligned buffer");
+  return launched(rq::launch_pack_q4_scales(src, rows, D, group, (int)eb, dst, stream), "rq_pack_q4_scales");
+}
+
+size_t rq_q4_matvec_workspace(const rq_q4_matrix* W, int32_t x_dtype, int32_t prologue, int32_t B) {
+  if (check_q4_call(W, x_dtype, prologue, B) != RQ_OK || B == 0 || W->rows == 0) return 0;
+  return rq::q4_matvec_ws_bytes(W, x_dtype, prologue == RQ_PRO_GELU_TANH_MUL, B);
+}
+
+rq_status rq_q4_matvec(const rq_q4_matrix* W, const void* x, int32_t x_dtype, const float* x2, int32_t prologue, int32_t B,
+                       float* y, void* ws, size_t ws_bytes, hipStream_t stream) {
+  CallRange range(__func__);
+  rq_status s = check_q4_call(W, x_dtype, prologue, B);
+  if (s != RQ_OK) return s;
+  if (B == 0 || W->rows == 0) return RQ_OK;
+  if (!W->codes || !W->scales) return fail(RQ_ERR_NULL, "4-bit matrix: codes or scales is NULL");
+  if (!aligned(W->codes, 16) || !aligned(W->scales, 16) || !aligned(W->offsets, 16) || !aligned(W->levels, 4))
+    return fail(RQ_ERR_ALIGN, "4-bit matrix: codes, scales and offsets must be 16-byte aligned, levels 4-byte aligned");
+  const bool two = prologue == RQ_PRO_GELU_TANH_MUL;
+  if (!x || !y || (two && !x2)) return fail(RQ_ERR_NULL, "q4_matvec: NULL buffer");
+  if (!aligned(x, dtype_bytes(x_dtype)) || !aligned(y, 4) || (two && !aligned(x2, 4)))
+    return fail(RQ_ERR_ALIGN, "q4_matvec: misaligned buffer");
+  const size_t need = rq::q4_matvec_ws_bytes(W, x_dtype, two, B);
+  if (need > 0) {
+    if (!ws || ws_bytes < need) return fail(RQ_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws ? ws_bytes : 0, need);
+    if (!aligned(ws, 256)) return fail(RQ_ERR_ALIGN, "workspace must be 256-byte aligned");
+  }
+  return launched(rq::launch_q4_matvec(W, x, x_dtype, two ? x2 : nullptr, B, y, ws, stream), "rq_q4_matvec");
+}
+
+rq_status rq_rope(const void* x, int32_t x_dtype, int32_t tokens, int32_t heads, int32_t head_dim, int64_t x_stride,
+                  const int32_t* positions, const double* freqs, int32_t rot, int32_t layout, float mscale, int32_t inverse,
+                  void* out, int32_t out_dtype, int64_t out_stride, hipStream_t stream) {
+  CallRange range(__func__);
+  rq_status s = check_heads(heads, head_dim);
+  if (s == RQ_OK) s = check_tokens(tokens, heads);
+  if (s != RQ_OK) return s;
+  if (!any_dtype(x_dtype) || !any_dtype(out_dtype)) return fail(RQ_ERR_DTYPE, "unknown dtype %d or %d", x_dtype, out_dtype);
+  s = check_stride("rope: x", x_stride, heads, head_dim);
+  if (s == RQ_OK) s = check_stride("rope: out", out_stride, heads, head_dim);
+  if (s == RQ_OK) s = check_rotation(rot, head_dim, layout, freqs, positions);
+  if (s != RQ_OK) return s;
+  if (tokens == 0) return RQ_OK;
+  if (!x || !out || !positions) return fail(RQ_ERR_NULL, "rope: NULL buffer");
+  if (!aligned(x, dtype_bytes(x_dtype)) || !aligned(out, dtype_bytes(out_dtype)))
+    return fail(RQ_ERR_ALIGN, "rope: x or out misaligned");
+  if (x == out && (x_dtype != out_dtype || x_stride != out_stride))
+    return fail(RQ_ERR_SHAPE, "rope: in place needs one type and one stride");
+  return launched(rq::launch_rope(x, x_dtype, tokens, heads, head_dim, x_stride, positions, freqs, rot, layout, mscale,
+                                  inverse != 0, out, out_dtype, out_stride, stream),
+                  "rq_rope");
+}
+
+rq_status rq_rope_append(const rq_seq_batch* batch, const rq_kv_cache* cache, const void* q, const void* k, const void* v,
+                         int32_t in_dtype, int64_t q_stride, int64_t k_stride, int64_t v_stride, int32_t heads,
+                         const int32_t* positions, const double* freqs, int32_t rot, int32_t layout, float mscale,
+                         void* q_out, int32_t* bad_pages, hipStream_t stream) {
+  CallRange range(__func__);
+  rq_status s = check_cache(cache);
+  if (s == RQ_OK) s = check_heads(heads, cache->head_dim);
+  if (s != RQ_OK) return s;
+  if (heads % cache->kv_heads) return fail(RQ_ERR_SHAPE, "heads=%d is no multiple of kv_heads=%d", heads, cache->kv_heads);
+  s = check_batch(batch, heads);
+  if (s != RQ_OK) return s;
+  if (!any_dtype(in_dtype)) return fail(RQ_ERR_DTYPE, "unknown dtype %d", in_dtype);
+  s = check_stride("rope_append: q", q_stride, heads, cache->head_dim);
+  if (s == RQ_OK) s = check_stride("rope_append: k", k_stride, cache->kv_heads, cache->head_dim);
+  if (s == RQ_OK) s = check_stride("rope_append: v", v_stride, cache->kv_heads, cache->head_dim);
+  if (s == RQ_OK) s = check_rotation(rot, cache->head_dim, layout, freqs, positions);
+  if (s != RQ_OK) return s;
+  if (batch->seqs == 0 || batch->tokens == 0) return RQ_OK;
+  if (!q || !k || !v || !q_out) return fail(RQ_ERR_NULL, "rope_append: NULL buffer");
+  const size_t eb = dtype_bytes(in_dtype);
+  if (!aligned(q, eb) || !aligned(k, eb) || !aligned(v, eb) || !aligned(q_out, 2) || !aligned(bad_pages, 4))
+    return fail(RQ_ERR_ALIGN, "rope_append: misaligned buffer");
+  if (q_out == q || q_out == k || q_out == v) return fail(RQ_ERR_SHAPE, "rope_append: q_out must not be an input");
+  return launched(rq::launch_rope_append(batch, cache, q, k, v, in_dtype, q_stride, k_stride, v_stride, heads, positions,
+                                         freqs, rot, layout, mscale, q_out, bad_pages, stream),
+                  "rq_rope_append");
+}
+
+size_t rq_paged_attn_workspace(const rq_kv_cache* cache, int32_t tokens, int32_t seqs, int32_t heads, int32_t max_len) {
+  if (check_attn_call(cache, tokens, seqs, heads, max_len) != RQ_OK || tokens == 0 || seqs == 0) return 0;
+  return rq::paged_attn_ws_bytes(cache, tokens, seqs, heads, max_len > 0 ? max_len : 1 << 30);
+}
+
+rq_status rq_paged_attn(const rq_seq_batch* batch, const rq_kv_cache* cache, const void* q, int64_t q_stride, int32_t heads,
+                        float scale, float softcap, int32_t window, int32_t max_len, void* out, float* lse,
+                        int32_t* bad_pages, void* ws, size_t ws_bytes, hipStream_t stream) {
+  CallRange range(__func__);
+  rq_status s = check_cache(cache);
+  if (s == RQ_OK) s = check_batch(batch, heads < 1 ? 1 : heads);
+  if (s == RQ_OK) s = check_attn_call(cache, batch->tokens, batch->seqs, heads, max_len);
+  if (s == RQ_OK) s = check_stride("paged_attn: q", q_stride, heads, cache->head_dim);
+  if (s != RQ_OK) return s;
+  if (window < 0) return fail(RQ_ERR_SHAPE, "window=%d < 0", window);
+  if (batch->seqs == 0 || batch->tokens == 0) return RQ_OK;
+  if (!q || !out) return fail(RQ_ERR_NULL, "paged_attn: NULL buffer");
+  if (q == out) return fail(RQ_ERR_SHAPE, "paged_attn: out must not be q");
+  if (!aligned(q, 16) || q_stride % 8 || !aligned(out, 16) || !aligned(lse, 4) || !aligned(bad_pages, 4))
+    return fail(RQ_ERR_ALIGN, "paged_attn: q and out must be 16-byte aligned, q_stride a multiple of 8");
+  const int32_t bound = max_len > 0 ? max_len : 1 << 30;
+  const size_t need = rq::paged_attn_ws_bytes(cache, batch->tokens, batch->seqs, heads, bound);
+  if (need > 0) {
+    if (!ws || ws_bytes < need) return fail(RQ_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws ? ws_bytes : 0, need);
+    if (!aligned(ws, 256)) return fail(RQ_ERR_ALIGN, "workspace must be 256-byte aligned");
+  }
+  return launched(rq::launch_paged_attn(batch, cache, q, q_stride, heads, scale, softcap, window, bound, out, lse, bad_pages,
+                                        ws, stream),
+                  "rq_paged_attn");
+}
+
+}  // extern "C"
+
 namespace {
 
 constexpr int kMaxDevices = 64;

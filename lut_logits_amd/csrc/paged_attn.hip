@@ -1,0 +1,773 @@
+// paged_attn.hip -- attention of each sequence's newest tokens over its paged cache.
+//
+//     o[t][h] = sum_j p_j v_j / sum_j p_j,   p_j = exp(z_j - max z),   z_j = cap * tanh(scale q.k_j / cap)   (cap <= 0: scale q.k_j)
+// over the keys j <= place(t), j > place(t) - window; one pass over the keys with a running maximum and sum (base 2, fp32).
+//
+// Rows: the query heads of one kv head are rows of the same tile, row = token * group + head in the group, so the cache
+// is read once for all of them.
+//
+// Orientation: both products are taken transposed, S^T = K Q^T and O^T = V^T P^T. The matrix core's result layout then
+// gives a lane four consecutive keys of ONE query row; with the rows of the K operand permuted (key_of_row) these become eight
+// consecutive keys, which is the operand layout of P^T: the probabilities never leave the registers,
+// maxima and sums need one or two lane exchanges, and the rescaling factor is the lane's own. V is kept transposed in its
+// pages, so its operand is eight consecutive keys of a column: 16 bytes, as K's are.
+//
+// Two kernels by the rows a sequence brings (launch_paged_attn):
+// - rows_kernel, 16 rows (decode, drafts): HBM bound on the cache. Each of 4 waves takes every fourth tile of 32 keys straight from
+//   memory into operand registers; the next tile's K is requested as soon as the current one's has been used, and V one step later.
+//   P is split in two parts of 16 bits: the matrix cores are idle anyway and the result is then exact to the output's rounding.
+// - tile_kernel, 128 rows (chunks, prompts): matrix-core bound. 4 waves of 32 rows share tiles of 64 keys (32 at head size 256)
+//   that go straight from memory to LDS, double buffered, one barrier a tile. P is rounded once to the cache's type.
+// Both split the keys over workgroups (the grid's second axis) when there are too few rows to fill the chip; the parts are joined by join_kernel
+// in a fixed order: no atomics, the same call gives the same bits.
+//
+// Keys that no row of a tile sees (places past the end, stale pages, before the window) are not multiplied: their V is set to zero
+// bits and their scores to -inf whatever the memory holds. A tile whose visible V holds infinities or NaN and that not all rows see
+// alike goes key by key (careful_pv), so that such a value reaches only the rows that see it.
+#include "rq_internal.h"
+
+namespace rq {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float floatx4 __attribute__((ext_vector_type(4)));
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kNegInf = -__builtin_huge_valf();
+constexpr int kThreads = 256;
+constexpr int kRowsSmall = 16, kRowsTile = 128;
+constexpr int kSplitKeys = 128;   // keys come in blocks of this size when they are split over workgroups
+
+struct AttnArgs {
+  const uint16_t* q;
+  int64_t q_stride;
+  rq_seq_batch batch;
+  rq_kv_cache cache;
+  int heads, group;            // query heads, and of one kv head
+  int page_shift;
+  int rows;                    // rows of a tile
+  float z_scale, cap_in, cap_out;   // base-2 scores: z * z_scale, or cap_out * tanh(z * cap_in)
+  int window;
+  int splits;
+  uint16_t* out;               // [tokens][heads][size]
+  float* lse;                  // [tokens][heads], or null
+  float* part_o;               // [tokens][heads][splits][size]
+  float2* part_ml;             // [tokens][heads][splits]: base-2 maximum, sum
+  int32_t* bad;
+};
+
+// A tile of rows of one sequence, and the blocks of keys [blk0, blk0 + per) of its split.
+struct RowTile {
+  int t0, n;                   // the sequence's first token (row of q) and its number of tokens
+  int row0, rows;              // the tile's rows: row0 .. row0 + rows - 1 of n * group
+  int place0;                  // place of the sequence's first new token (may be negative)
+  int seq;
+  int key_lo, key_hi;          // keys that some row sees: key_lo .. key_hi (none: key_hi < key_lo)
+  int per, active;             // blocks of keys a split, splits with any
+};
+
+__device__ __forceinline__ RowTile row_tile(const AttnArgs& a, const SeqTile& st) {
+  RowTile r;
+  r.seq = st.seq;
+  r.t0 = st.t0;
+  r.n = st.n;
+  r.place0 = st.len - st.n;
+  r.row0 = st.tile * a.rows;
+  r.rows = min(a.rows, st.n * a.group - r.row0);
+  if (r.rows <= 0) return r;
+  const int first = r.place0 + r.row0 / a.group, last = r.place0 + (r.row0 + r.rows - 1) / a.group;
+  const int capacity = (int)min((int64_t)a.batch.max_pages << a.page_shift, (int64_t)1 << 30);
+  r.key_hi = min(last, capacity - 1);
+  r.key_lo = a.window > 0 ? max(0, first - a.window + 1) : 0;
+  const int blocks = r.key_hi < r.key_lo ? 0 : r.key_hi / kSplitKeys - r.key_lo / kSplitKeys + 1;
+  r.per = (blocks + a.splits - 1) / a.splits;
+  r.active = r.per ? (blocks + r.per - 1) / r.per : 0;
+  return r;
+}
+
+// keys [lo, hi) of split z
+__device__ __forceinline__ void split_range(const RowTile& r, int z, int& lo, int& hi) {
+  const int b = r.key_lo / kSplitKeys;
+  lo = max(r.key_lo, (b + z * r.per) * kSplitKeys);
+  hi = (int)min((int64_t)r.key_hi + 1, (int64_t)(b + (z + 1) * r.per) * kSplitKeys);
+}
+
+// The page of a key, or -1 if the table has none or a bad one.
+__device__ __forceinline__ int page_of(const AttnArgs& a, const int32_t* table, int key) {
+  const int i = key >> a.page_shift;
+  if (i >= a.batch.max_pages) return -1;
+  const int p = table[i];
+  return (unsigned)p < (unsigned)a.cache.pages ? p : -1;
+}
+
+template <bool F16>
+struct Type {
+  typedef bf16x8 vec;
+  static __device__ __forceinline__ uint32_t round2(float a, float b) {
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{a, b}, b2));
+  }
+  static __device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
+  static __device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+  static __device__ __forceinline__ floatx4 mfma16(u32x4 a, u32x4 b, floatx4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ floatx16 mfma32(u32x4 a, u32x4 b, floatx16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  }
+  static constexpr uint32_t kExp = 0x7f80u;
+};
+template <>
+struct Type<true> {
+  static __device__ __forceinline__ uint32_t round2(float a, float b) {
+    const uint16_t x = __builtin_bit_cast(uint16_t, (_Float16)a), y = __builtin_bit_cast(uint16_t, (_Float16)b);
+    return x | ((uint32_t)y << 16);
+  }
+  static __device__ __forceinline__ float lo(uint32_t w) { return (float)__builtin_bit_cast(_Float16, (uint16_t)w); }
+  static __device__ __forceinline__ float hi(uint32_t w) { return (float)__builtin_bit_cast(_Float16, (uint16_t)(w >> 16)); }
+  static __device__ __forceinline__ floatx4 mfma16(u32x4 a, u32x4 b, floatx4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ floatx16 mfma32(u32x4 a, u32x4 b, floatx16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  }
+  static constexpr uint32_t kExp = 0x7c00u;
+};
+
+// Base-2 score of a product q.k. tanh(u) = 1 - 2 / (1 + e^2u): its absolute error of 1e-7 is 1e-5 of a
+// probability at a cap of 50, far below the rounding of 16-bit outputs.
+__device__ __forceinline__ float score(const AttnArgs& a, float z) {
+  if (a.cap_out > 0.0f) {   // (uniform)
+    const float e = __builtin_amdgcn_exp2f(z * a.cap_in * (2.0f * kLog2e));
+    return a.cap_out * (1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + e));
+  }
+  return z * a.z_scale;
+}
+
+// Whether a word holds an infinity or NaN in either half.
+template <bool F16>
+__device__ __forceinline__ bool not_finite(uint32_t w) {
+  constexpr uint32_t m = Type<F16>::kExp;
+  return (w & m) == m || (w & (m << 16)) == (m << 16);
+}
+
+// ---------------------------------------------------------------- few rows
+
+template <int DH, bool F16>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 8))) void attn_rows_kernel(AttnArgs a) {
+  typedef Type<F16> Ty;
+  constexpr int KS = DH / 32;   // steps of q.k
+  constexpr int DT = DH / 16;   // column tiles of V
+  __shared__ float2 ml[4][kRowsSmall];
+  extern __shared__ __align__(16) float osh[];   // [4][16][DH + 4]
+  constexpr int OLD = DH + 4;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int i16 = lane & 15, kg = lane >> 4;
+  // kv heads are the fastest index: workgroups go round the XCDs in order, so that with 8 kv heads (or 4) one's cache meets one (or two) L2s
+  const int slot = (int)blockIdx.x / a.cache.kv_heads, kvh = (int)blockIdx.x - slot * a.cache.kv_heads, split = blockIdx.y;
+  const SeqTile st = find_tile_rows(a.batch, a.rows, a.group, slot);
+  if (st.seq < 0) return;
+  const RowTile r = row_tile(a, st);
+  if (r.rows <= 0) return;
+  const bool none = r.active == 0;                 // no row sees a key: zeros, by split 0
+  if (none ? split > 0 : split >= r.active) return;
+
+  // this lane's row (rows past the tile repeat its last one and are not stored)
+  const int row = r.row0 + min(i16, r.rows - 1);
+  const int tok = row / a.group;
+  const int head = kvh * a.group + row - tok * a.group;
+  const int place = r.place0 + tok;
+  u32x4 qf[KS];
+  {
+    const uint16_t* qp = a.q + (int64_t)(r.t0 + tok) * a.q_stride + (int64_t)head * DH + 8 * kg;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) qf[s] = *reinterpret_cast<const u32x4*>(qp + 32 * s);
+  }
+  floatx4 o[DT];
+#pragma unroll
+  for (int d = 0; d < DT; ++d) o[d] = floatx4{0.f, 0.f, 0.f, 0.f};
+  float m = kNegInf, l = 0.0f;
+
+  if (!none) {
+    int lo, hi;
+    split_range(r, split, lo, hi);
+    const int32_t* table = a.batch.table + (int64_t)r.seq * a.batch.max_pages;
+    // places of the tile's first and last row
+    const int place_a = r.place0 + r.row0 / a.group, place_b = r.place0 + (r.row0 + r.rows - 1) / a.group;
+    const int64_t page_elems = (int64_t)a.cache.kv_heads << a.page_shift;   // * DH
+    const int pmask = (1 << a.page_shift) - 1;
+    const uint16_t* kbase = static_cast<const uint16_t*>(a.cache.k) + ((int64_t)kvh << a.page_shift) * DH;
+    const uint16_t* vbase = static_cast<const uint16_t*>(a.cache.v) + ((int64_t)kvh << a.page_shift) * DH;
+    const int krow = 8 * (i16 >> 2) + (i16 & 3);   // this lane's key of sub-tile 0 (sub-tile 1: + 4)
+    const int t_end = (hi + 31) / 32;
+    u32x4 kf[2][KS], vf[DT];
+    // the two halves of a tile of 32 keys may lie in two pages of 16
+    auto pages = [&](int t, int& p0, int& p1) {
+      p0 = page_of(a, table, 32 * t);
+      p1 = page_of(a, table, 32 * t + 16);
+    };
+    auto load_k = [&](int t, int p0, int p1) {
+      const int p = max(0, krow < 16 ? p0 : p1);
+      const uint16_t* kp = kbase + p * page_elems * DH + (int64_t)((32 * t + krow) & pmask) * DH + 8 * kg;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int s = 0; s < KS; ++s) kf[u][s] = *reinterpret_cast<const u32x4*>(kp + u * 4 * DH + 32 * s);
+    };
+    auto load_v = [&](int t, int p0, int p1) {
+      const int p = max(0, kg < 2 ? p0 : p1);
+      const uint16_t* vp = vbase + p * page_elems * DH + ((int64_t)i16 << a.page_shift) + ((32 * t + 8 * kg) & pmask);
+#pragma unroll
+      for (int d = 0; d < DT; ++d) vf[d] = *reinterpret_cast<const u32x4*>(vp + ((int64_t)(16 * d) << a.page_shift));
+    };
+    int t = lo / 32 + wave;
+    int p0 = -1, p1 = -1, n0 = -1, n1 = -1;
+    if (t < t_end) {
+      pages(t, p0, p1);
+      load_k(t, p0, p1);
+      load_v(t, p0, p1);
+      if (t + 4 < t_end) pages(t + 4, n0, n1);
+    }
+    for (; t < t_end; t += 4) {
+      floatx4 s[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        s[u] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < KS; ++k) s[u] = Ty::mfma16(kf[u][k], qf[k], s[u]);
+      }
+      const bool more = t + 4 < t_end;
+      if (more) load_k(t + 4, n0, n1);
+      // s[u][e]: key 32 t + 8 kg + 4 u + e of this lane's row
+      const int key0 = 32 * t + 8 * kg;
+      const bool pages_ok = p0 >= 0 && p1 >= 0;
+      const bool whole = pages_ok && 32 * t >= lo && 32 * t + 31 < hi && 32 * t + 31 <= place_a &&
+                         (a.window <= 0 || 32 * t > place_b - a.window);   // every row sees every key
+      float z[8];
+      uint32_t seen = 0xffu;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[j] = score(a, s[j >> 2][j & 3]);
+      if (!whole) {   // (uniform)
+        const bool ok = (kg < 2 ? p0 : p1) >= 0;
+        seen = 0;
+        uint32_t any = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int key = key0 + j;
+          const bool in = ok && key >= lo && key < hi;
+          if (in) any |= 1u << j;
+          if (in && key <= place && (a.window <= 0 || key > place - a.window)) seen |= 1u << j;
+          if (!(seen >> j & 1)) z[j] = kNegInf;
+        }
+        // V of keys that are no one's: zero bits
+        u32x4 keep;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          keep[j] = ((any >> (2 * j)) & 1u ? 0xffffu : 0u) | ((any >> (2 * j + 1)) & 1u ? 0xffff0000u : 0u);
+#pragma unroll
+        for (int d = 0; d < DT; ++d) vf[d] &= keep;
+      }
+      float mt = z[0];
+#pragma unroll
+      for (int j = 1; j < 8; ++j) mt = fmaxf(mt, z[j]);
+      mt = fmaxf(mt, __shfl_xor(mt, 16, 64));
+      mt = fmaxf(mt, __shfl_xor(mt, 32, 64));
+      const float mn = fmaxf(m, mt);
+      const float mu = mn == kNegInf ? 0.0f : mn;
+      if (__any(mn > m)) {   // some row's maximum grew
+        const float f = __builtin_amdgcn_exp2f(m - mu);
+        l *= f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[d] *= f;
+        m = mn;
+      }
+      u32x4 ph, pl;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float x = __builtin_amdgcn_exp2f(z[2 * j] - mu), y = __builtin_amdgcn_exp2f(z[2 * j + 1] - mu);
+        l += x + y;
+        ph[j] = Ty::round2(x, y);
+        pl[j] = Ty::round2(x - Ty::lo(ph[j]), y - Ty::hi(ph[j]));
+      }
+      // (also where every row sees every key: an infinity must not meet the zeros of P's low part)
+      bool wild = false;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) wild |= not_finite<F16>(vf[d][j]);
+      wild = __any(wild);
+      if (wild) {   // key by key: a row takes only what it sees
+        for (int k = 0; k < 32; ++k) {
+          const uint32_t word = (k & 7) >> 1, half = (k & 1) ? 0xffff0000u : 0xffffu;
+          const bool mine = kg == k >> 3;
+          u32x4 pk, plk, keep;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            keep[j] = mine && (uint32_t)j == word ? half : 0u;
+            pk[j] = ph[j] & keep[j];
+            plk[j] = pl[j] & keep[j];
+          }
+          const bool sees = __shfl((int)(seen >> (k & 7)) & 1, i16 + 16 * (k >> 3), 64);
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+            const u32x4 vk = vf[d] & keep;
+            // the low part of P only meets finite values (inf * 0 would be NaN)
+            u32x4 fin;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) fin[j] = not_finite<F16>(vk[j]) ? 0u : vk[j];
+            const floatx4 with = Ty::mfma16(fin, plk, Ty::mfma16(vk, pk, o[d]));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[d][e] = sees ? with[e] : o[d][e];
+          }
+        }
+      } else {
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[d] = Ty::mfma16(vf[d], pl, Ty::mfma16(vf[d], ph, o[d]));
+      }
+      if (more) {
+        load_v(t + 4, n0, n1);
+        p0 = n0;
+        p1 = n1;
+        if (t + 8 < t_end) pages(t + 8, n0, n1);
+      }
+    }
+    l += __shfl_xor(l, 16, 64);
+    l += __shfl_xor(l, 32, 64);
+  }
+
+  // join the waves: rows' maxima and sums, then the outputs, in wave order
+  if (kg == 0) ml[wave][i16] = make_float2(m, l);
+#pragma unroll
+  for (int d = 0; d < DT; ++d) *reinterpret_cast<floatx4*>(osh + ((size_t)wave * 16 + i16) * OLD + 16 * d + 4 * kg) = o[d];
+  __syncthreads();
+  for (int i = tid; i < r.rows * (DH / 4); i += kThreads) {
+    const int rr = i / (DH / 4), c = (i - rr * (DH / 4)) * 4;
+    float mm = kNegInf;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) mm = fmaxf(mm, ml[w][rr].x);
+    const float mu = mm == kNegInf ? 0.0f : mm;
+    float ll = 0.0f;
+    floatx4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float f = __builtin_amdgcn_exp2f(ml[w][rr].x - mu);
+      ll += f * ml[w][rr].y;
+      v += f * *reinterpret_cast<const floatx4*>(osh + ((size_t)w * 16 + rr) * OLD + c);
+    }
+    const int grow = r.row0 + rr, tk = grow / a.group;
+    const int64_t th = (int64_t)(r.t0 + tk) * a.heads + kvh * a.group + grow - tk * a.group;
+    if (a.splits > 1) {   // (uniform)
+      *reinterpret_cast<floatx4*>(a.part_o + (th * a.splits + split) * DH + c) = v;
+      if (c == 0) a.part_ml[th * a.splits + split] = make_float2(mm, ll);
+    } else {
+      const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+      *reinterpret_cast<u32x2*>(a.out + th * DH + c) = u32x2{Ty::round2(v[0] * inv, v[1] * inv), Ty::round2(v[2] * inv, v[3] * inv)};
+      if (c == 0 && a.lse) a.lse[th] = ll == 0.0f ? kNegInf : (mm + log2f(ll)) * kLn2;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- many rows
+
+template <int DH>
+constexpr int tile_keys() { return DH == 256 ? 32 : 64; }
+
+// Row of a 32-row operand tile -> key: the two middle bits of each 16 change places, so that a lane's result rows
+// (4h .. 4h+3 and 8+4h .. 8+4h+3) are the eight consecutive keys 8h .. 8h+7.
+__device__ __forceinline__ int key_of_row(int i) { return (i & ~12) | ((i & 4) << 1) | ((i & 8) >> 1); }
+
+template <int DH, bool F16>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))) void attn_tile_kernel(AttnArgs a) {
+  typedef Type<F16> Ty;
+  constexpr int BK = tile_keys<DH>();
+  constexpr int NS = BK / 32;        // key sub-tiles of 32
+  constexpr int KS = DH / 16;        // steps of q.k
+  constexpr int DT = DH / 32;        // column tiles of V
+  constexpr int KC = DH / 8;         // 16-byte chunks of a K row
+  constexpr int VC = BK / 8;         // and of a V row
+  constexpr int CH = BK * DH / 8;    // chunks of a K (or V) tile
+  constexpr int PG = BK / 16;        // pages a tile may touch
+  extern __shared__ __align__(16) unsigned char smem[];   // 2 x { K [BK][DH], V [DH][BK] }, chunks swizzled
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int i32 = lane & 31, h = lane >> 5;
+  // last tiles first: under the causal mask they are the longest
+  const int slot = (int)blockIdx.x / a.cache.kv_heads, kvh = (int)blockIdx.x - slot * a.cache.kv_heads, split = blockIdx.y;
+  const SeqTile st = find_tile_rows(a.batch, a.rows, a.group, (int)gridDim.x / a.cache.kv_heads - 1 - slot);
+  if (st.seq < 0) return;
+  const RowTile r = row_tile(a, st);
+  if (r.rows <= 0) return;
+  const bool none = r.active == 0;
+  if (none ? split > 0 : split >= r.active) return;
+
+  const int wrow = min(r.row0 + 32 * wave, r.row0 + r.rows - 1);            // the wave's first row
+  const int wlast = min(r.row0 + 32 * wave + 31, r.row0 + r.rows - 1);      // and last
+  const bool idle = 32 * wave >= r.rows;                                     // no row of its own: it only copies
+  const int row = min(r.row0 + 32 * wave + i32, r.row0 + r.rows - 1);
+  const int tok = row / a.group;
+  const int head = kvh * a.group + row - tok * a.group;
+  const int place = r.place0 + tok;
+  u32x4 qf[KS];
+  {
+    const uint16_t* qp = a.q + (int64_t)(r.t0 + tok) * a.q_stride + (int64_t)head * DH + 8 * h;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) qf[s] = *reinterpret_cast<const u32x4*>(qp + 16 * s);
+  }
+  floatx16 o[DT];
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[d][e] = 0.0f;
+  float m = kNegInf, l = 0.0f;
+
+  if (!none) {
+    int lo, hi;
+    split_range(r, split, lo, hi);
+    const int32_t* table = a.batch.table + (int64_t)r.seq * a.batch.max_pages;
+    const int place_a = r.place0 + wrow / a.group, place_b = r.place0 + wlast / a.group;
+    const int64_t page_elems = ((int64_t)a.cache.kv_heads << a.page_shift) * DH;
+    const int pmask = (1 << a.page_shift) - 1;
+    const uint16_t* kbase = static_cast<const uint16_t*>(a.cache.k) + ((int64_t)kvh << a.page_shift) * DH;
+    const uint16_t* vbase = static_cast<const uint16_t*>(a.cache.v) + ((int64_t)kvh << a.page_shift) * DH;
+    auto pages = [&](int t, int (&p)[PG]) {
+#pragma unroll
+      for (int i = 0; i < PG; ++i) p[i] = page_of(a, table, BK * t + 16 * i);
+    };
+    auto page_at = [&](const int (&p)[PG], int off) {   // off: key - BK t
+      int x = p[0];
+#pragma unroll
+      for (int i = 1; i < PG; ++i) x = off >= 16 * i ? p[i] : x;
+      return max(0, x);
+    };
+    // copies tile t into buffer b: 16 bytes a lane, lane after lane in LDS, so the swizzle is in what each lane fetches
+    auto copy = [&](int b, int t, const int (&p)[PG]) {
+      unsigned char* kd = smem + (size_t)b * 2 * CH * 16;
+      unsigned char* vd = kd + (size_t)CH * 16;
+#pragma unroll
+      for (int j = 0; j < CH / kThreads; ++j) {
+        const int c = j * kThreads + tid;
+        const int i = c / KC, ch = (c % KC) ^ (i & 7);
+        const int off = key_of_row(i);
+        const uint16_t* src = kbase + page_at(p, off) * page_elems + (int64_t)((BK * t + off) & pmask) * DH + 8 * ch;
+        __builtin_amdgcn_global_load_lds((const void*)src, (lds_ptr_t)(kd + (size_t)(j * kThreads + wave * 64) * 16), 16, 0, 0);
+      }
+#pragma unroll
+      for (int j = 0; j < CH / kThreads; ++j) {
+        const int c = j * kThreads + tid;
+        const int i = c / VC;
+        const int ch = (c % VC) ^ (VC == 8 ? (i & 7) : ((i >> 1) & 3));
+        const uint16_t* src = vbase + page_at(p, 8 * ch) * page_elems + ((int64_t)i << a.page_shift) + ((BK * t + 8 * ch) & pmask);
+        __builtin_amdgcn_global_load_lds((const void*)src, (lds_ptr_t)(vd + (size_t)(j * kThreads + wave * 64) * 16), 16, 0, 0);
+      }
+    };
+    const int t0 = lo / BK, t_end = (hi + BK - 1) / BK;
+    int p[PG], pn[PG];
+    pages(t0, p);
+    copy(0, t0, p);
+#pragma unroll
+    for (int i = 0; i < PG; ++i) pn[i] = p[i];
+    if (t0 + 1 < t_end) pages(t0 + 1, pn);
+    for (int t = t0; t < t_end; ++t) {
+      const int b = (t - t0) & 1;
+      __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): this wave's copies of the tile have landed
+      __syncthreads();                      // and everyone's; the other buffer has been read
+      if (t + 1 < t_end) copy(b ^ 1, t + 1, pn);
+      const bool hidden = idle || BK * t > place_b || (a.window > 0 && BK * t + BK - 1 <= place_a - a.window);
+      if (!hidden) {   // (uniform)
+        const unsigned char* kl = smem + (size_t)b * 2 * CH * 16;
+        const unsigned char* vl = kl + (size_t)CH * 16;
+        bool ok = true;
+#pragma unroll
+        for (int i = 0; i < PG; ++i) ok = ok && p[i] >= 0;
+        const bool whole = ok && BK * t >= lo && BK * t + BK - 1 < hi && BK * t + BK - 1 <= place_a &&
+                           (a.window <= 0 || BK * t > place_b - a.window);
+        floatx16 s[NS];
+#pragma unroll
+        for (int u = 0; u < NS; ++u) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) s[u][e] = 0.0f;
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            const int i = 32 * u + i32;
+            const u32x4 kf = *reinterpret_cast<const u32x4*>(kl + ((size_t)i * KC + ((2 * k + h) ^ (i & 7))) * 16);
+            s[u] = Ty::mfma32(kf, qf[k], s[u]);
+          }
+        }
+        // s[u][8 g + j]: key BK t + 32 u + 16 g + 8 h + j of this lane's row
+        uint32_t seen[NS], any[NS];   // bit 8 g + j
+        float mt = kNegInf;
+#pragma unroll
+        for (int u = 0; u < NS; ++u) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) s[u][e] = score(a, s[u][e]);
+          seen[u] = any[u] = 0xffffu;
+          if (!whole) {   // (uniform)
+            seen[u] = any[u] = 0;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int key = BK * t + 32 * u + 16 * (e >> 3) + 8 * h + (e & 7);
+              const bool in = p[2 * u + (e >> 3)] >= 0 && key >= lo && key < hi;
+              if (in) any[u] |= 1u << e;
+              if (in && key <= place && (a.window <= 0 || key > place - a.window)) seen[u] |= 1u << e;
+              if (!(seen[u] >> e & 1)) s[u][e] = kNegInf;
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e) mt = fmaxf(mt, s[u][e]);
+        }
+        mt = fmaxf(mt, __shfl_xor(mt, 32, 64));
+        const float mn = fmaxf(m, mt);
+        const float mu = mn == kNegInf ? 0.0f : mn;
+        if (__any(mn > m)) {
+          const float f = __builtin_amdgcn_exp2f(m - mu);
+          l *= f;
+#pragma unroll
+          for (int d = 0; d < DT; ++d) o[d] *= f;
+          m = mn;
+        }
+        u32x4 pf[NS][2];
+#pragma unroll
+        for (int u = 0; u < NS; ++u)
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float x = __builtin_amdgcn_exp2f(s[u][8 * g + 2 * j] - mu), y = __builtin_amdgcn_exp2f(s[u][8 * g + 2 * j + 1] - mu);
+              l += x + y;
+              pf[u][g][j] = Ty::round2(x, y);   // rounded to the cache's type: half a step of each probability
+            }
+        auto v_at = [&](int d, int u, int g) {
+          const int i = 32 * d + i32, ch = 4 * u + 2 * g + h;
+          return *reinterpret_cast<const u32x4*>(vl + ((size_t)i * VC + (ch ^ (VC == 8 ? (i & 7) : ((i >> 1) & 3)))) * 16);
+        };
+        if (whole) {   // (uniform)
+#pragma unroll
+          for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int u = 0; u < NS; ++u)
+#pragma unroll
+              for (int g = 0; g < 2; ++g) o[d] = Ty::mfma32(v_at(d, u, g), pf[u][g], o[d]);
+        } else {
+#pragma unroll
+          for (int u = 0; u < NS; ++u)
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              u32x4 keep;   // V of keys that are no one's: zero bits
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                keep[j] = ((any[u] >> (8 * g + 2 * j)) & 1u ? 0xffffu : 0u) | ((any[u] >> (8 * g + 2 * j + 1)) & 1u ? 0xffff0000u : 0u);
+              bool wild = false;
+              u32x4 v[DT];
+#pragma unroll
+              for (int d = 0; d < DT; ++d) {
+                v[d] = v_at(d, u, g) & keep;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) wild |= not_finite<F16>(v[d][j]);
+              }
+              if (!__any(wild)) {
+#pragma unroll
+                for (int d = 0; d < DT; ++d) o[d] = Ty::mfma32(v[d], pf[u][g], o[d]);
+              } else {   // key by key: a row takes only what it sees
+                for (int k = 0; k < 16; ++k) {
+                  u32x4 mine;
+#pragma unroll
+                  for (int j = 0; j < 4; ++j)
+                    mine[j] = h == k >> 3 && j == (k & 7) >> 1 ? ((k & 1) ? 0xffff0000u : 0xffffu) : 0u;
+                  const bool sees = __shfl((int)(seen[u] >> (8 * g + (k & 7))) & 1, i32 + 32 * (k >> 3), 64);
+#pragma unroll
+                  for (int d = 0; d < DT; ++d) {
+                    const floatx16 with = Ty::mfma32(v[d] & mine, pf[u][g] & mine, o[d]);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[d][e] = sees ? with[e] : o[d][e];
+                  }
+                }
+              }
+            }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < PG; ++i) p[i] = pn[i];
+      if (t + 2 < t_end) pages(t + 2, pn);
+    }
+    l += __shfl_xor(l, 32, 64);
+  }
+  if (idle || 32 * wave + i32 >= r.rows) return;
+  const int64_t th = (int64_t)(r.t0 + tok) * a.heads + head;
+  // o[d][e]: column 32 d + 8 (e >> 2) + 4 h + (e & 3)
+  if (a.splits > 1) {   // (uniform)
+    float* po = a.part_o + (th * a.splits + split) * DH + 4 * h;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int e = 0; e < 16; e += 4)
+        *reinterpret_cast<floatx4*>(po + 32 * d + 2 * e) = floatx4{o[d][e], o[d][e + 1], o[d][e + 2], o[d][e + 3]};
+    if (h == 0) a.part_ml[th * a.splits + split] = make_float2(m, l);
+  } else {
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    uint16_t* op = a.out + th * DH + 4 * h;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int e = 0; e < 16; e += 4)
+        *reinterpret_cast<u32x2*>(op + 32 * d + 2 * e) =
+            u32x2{Ty::round2(o[d][e] * inv, o[d][e + 1] * inv), Ty::round2(o[d][e + 2] * inv, o[d][e + 3] * inv)};
+    if (h == 0 && a.lse) a.lse[th] = l == 0.0f ? kNegInf : (m + log2f(l)) * kLn2;
+  }
+}
+
+// ---------------------------------------------------------------- joining the splits
+
+// One wave a (token, head): the parts in split order. Tokens of no sequence are left as they are.
+template <int DH, bool F16>
+__global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a) {
+  constexpr int C = DH / 64;   // columns of a lane
+  const int lane = threadIdx.x & 63;
+  const int64_t th = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
+  if (th >= (int64_t)a.batch.tokens * a.heads) return;
+  const int t = (int)(th / a.heads);
+  SeqTile st = find_token(a.batch, t);
+  if (st.seq < 0) return;
+  const int row = (t - st.t0) * a.group + (int)(th - (int64_t)t * a.heads) % a.group;
+  st.tile = row / a.rows;
+  const RowTile r = row_tile(a, st);
+  const int n = max(1, r.active);   // a tile without keys is written by split 0
+  const float2* ml = a.part_ml + th * a.splits;
+  float mm = kNegInf;
+  for (int s = 0; s < n; ++s) mm = fmaxf(mm, ml[s].x);
+  const float mu = mm == kNegInf ? 0.0f : mm;
+  float ll = 0.0f, v[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) v[c] = 0.0f;
+  for (int s = 0; s < n; ++s) {
+    const float f = __builtin_amdgcn_exp2f(ml[s].x - mu);
+    ll += f * ml[s].y;
+    const float* po = a.part_o + (th * a.splits + s) * DH + lane * C;
+#pragma unroll
+    for (int c = 0; c < C; ++c) v[c] += f * po[c];
+  }
+  const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+  uint16_t* op = a.out + th * DH + lane * C;
+  if constexpr (C == 1) op[0] = (uint16_t)Type<F16>::round2(v[0] * inv, 0.0f);
+  else {
+#pragma unroll
+    for (int c = 0; c < C; c += 2) *reinterpret_cast<uint32_t*>(op + c) = Type<F16>::round2(v[c] * inv, v[c + 1] * inv);
+  }
+  if (lane == 0 && a.lse) a.lse[th] = ll == 0.0f ? kNegInf : (mm + log2f(ll)) * kLn2;
+}
+
+// Counts the tokens' sequences' pages that the table has none of: one thread a sequence and page in use.
+__global__ __launch_bounds__(kThreads) void attn_bad_kernel(rq_seq_batch b, rq_kv_cache cache, int32_t* bad) {
+  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (i >= (int64_t)b.seqs * b.max_pages) return;
+  const int s = (int)(i / b.max_pages), pi = (int)(i - (int64_t)s * b.max_pages);
+  if ((int64_t)pi * cache.page_size >= b.lens[s] || seq_begin(b, s) >= seq_begin(b, s + 1)) return;
+  if ((unsigned)b.table[i] >= (unsigned)cache.pages) atomicAdd(bad, 1);
+}
+
+struct AttnPlan {
+  int rows, splits;
+  int64_t slots;
+};
+
+// Rows of a tile by the rows a sequence brings on average, splits by how many workgroups the chip holds.
+AttnPlan plan_attn(const rq_kv_cache* c, int tokens, int seqs, int heads, int max_len) {
+  AttnPlan p;
+  const int group = heads / c->kv_heads;
+  const int64_t rows = (int64_t)tokens * group;
+  p.rows = rows <= (int64_t)kRowsSmall * 2 * seqs ? kRowsSmall : kRowsTile;
+  p.slots = rows / p.rows + seqs;
+  const int64_t each = (rows + seqs - 1) / seqs;   // rows of a sequence on average
+  const int64_t wgs = std::min<int64_t>(seqs, tokens) * ((each + p.rows - 1) / p.rows) * c->kv_heads;
+  const int64_t want = p.rows == kRowsSmall ? 4 * kCUs : 2 * kCUs;   // workgroups
+  const int64_t blocks = (max_len + kSplitKeys - 1) / kSplitKeys;
+  // a split takes at least 256 keys, so that joining stays cheap beside it
+  p.splits = (int)std::max<int64_t>(1, std::min({want / wgs, (blocks + 1) / 2, (int64_t)64}));
+  return p;
+}
+
+template <int DH, bool F16>
+hipError_t launch_dh(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
+  const dim3 grid((unsigned)(p.slots * a.cache.kv_heads), (unsigned)p.splits);
+  if (p.rows == kRowsSmall) {
+    const size_t lds = (size_t)4 * kRowsSmall * (DH + 4) * sizeof(float);
+    auto kern = attn_rows_kernel<DH, F16>;
+    if (lds > 64 * 1024) {
+      hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+      if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL(kern, grid, dim3(kThreads), lds, stream, a);
+  } else {
+    const size_t lds = (size_t)4 * tile_keys<DH>() * DH * sizeof(uint16_t);
+    hipLaunchKernelGGL((attn_tile_kernel<DH, F16>), grid, dim3(kThreads), lds, stream, a);
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.splits == 1) return e;
+  const int64_t n = ((int64_t)a.batch.tokens * a.heads + kThreads / 64 - 1) / (kThreads / 64);
+  hipLaunchKernelGGL((attn_join_kernel<DH, F16>), dim3((unsigned)n), dim3(kThreads), 0, stream, a);
+  return hipGetLastError();
+}
+
+template <bool F16>
+hipError_t launch_type(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
+  switch (a.cache.head_dim) {
+    case 64: return launch_dh<64, F16>(a, p, stream);
+    case 128: return launch_dh<128, F16>(a, p, stream);
+    default: return launch_dh<256, F16>(a, p, stream);
+  }
+}
+
+size_t part_o_bytes(const rq_kv_cache* c, int tokens, int heads, int splits) {
+  return (((size_t)tokens * heads * splits * c->head_dim * sizeof(float)) + 255) & ~(size_t)255;
+}
+
+}  // namespace
+
+size_t paged_attn_ws_bytes(const rq_kv_cache* c, int tokens, int seqs, int heads, int max_len) {
+  const AttnPlan p = plan_attn(c, tokens, seqs, heads, max_len);
+  if (p.splits == 1) return 0;
+  return part_o_bytes(c, tokens, heads, p.splits) + (size_t)tokens * heads * p.splits * sizeof(float2);
+}
+
+hipError_t launch_paged_attn(const rq_seq_batch* batch, const rq_kv_cache* cache, const void* q, int64_t q_stride, int heads,
+                             float scale, float softcap, int window, int max_len, void* out, float* lse, int32_t* bad,
+                             void* ws, hipStream_t stream) {
+  const AttnPlan p = plan_attn(cache, batch->tokens, batch->seqs, heads, max_len);
+  AttnArgs a = {};
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_stride = q_stride;
+  a.batch = *batch;
+  a.cache = *cache;
+  a.heads = heads;
+  a.group = heads / cache->kv_heads;
+  a.page_shift = __builtin_ctz((unsigned)cache->page_size);
+  a.rows = p.rows;
+  a.z_scale = scale * kLog2e;
+  a.cap_in = softcap > 0.0f ? scale / softcap : 0.0f;
+  a.cap_out = softcap > 0.0f ? softcap * kLog2e : 0.0f;
+  a.window = window;
+  a.splits = p.splits;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  a.part_o = static_cast<float*>(ws);
+  a.part_ml = p.splits > 1 ? reinterpret_cast<float2*>(static_cast<char*>(ws) +
+                                                       part_o_bytes(cache, batch->tokens, heads, p.splits))
+                           : nullptr;
+  a.bad = bad;
+  if (bad) {
+    const int64_t n = (int64_t)batch->seqs * batch->max_pages;
+    hipLaunchKernelGGL(attn_bad_kernel, dim3((unsigned)((n + kThreads - 1) / kThreads)), dim3(kThreads), 0, stream, *batch,
+                       *cache, bad);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return cache->dtype == RQ_F16 ? launch_type<true>(a, p, stream) : launch_type<false>(a, p, stream);
+}
+
+}  // namespace rq

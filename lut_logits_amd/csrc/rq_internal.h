@@ -79,6 +79,58 @@ inline int pairs_per_block(const rq_matrix* W) {
   return W->codes_layout == RQ_CODES_PACKED10 ? 12 : (W->codes_layout == RQ_CODES_PACKED8 ? 16 : 8);
 }
 
+// Sequences packed one behind the other (rq_seq_batch). First token of sequence s, kept inside the tokens
+// whatever cu_q holds.
+__device__ __forceinline__ int seq_begin(const rq_seq_batch& b, int s) { return min(max(b.cu_q[s], 0), b.tokens); }
+
+__device__ __forceinline__ int floor_div(int a, int b) { return a >= 0 ? a / b : -((b - 1 - a) / b); }
+
+struct SeqTile {
+  int seq;    // -1: none
+  int tile;   // the tile's number in the sequence (may lie behind its last)
+  int t0, n;  // the sequence's first token and number of tokens
+  int len;    // keys in the cache, the new ones among them
+};
+
+// The last sequence whose first slot (seq_begin * mul / div + extra * s) is at most idx, by the whole wave: 64 probes a step.
+__device__ __forceinline__ SeqTile find_slot(const rq_seq_batch& b, int mul, int div, int extra, int idx) {
+  SeqTile r;
+  r.seq = -1;
+  if (b.seqs <= 0) return r;
+  const int lane = threadIdx.x & 63;
+  int lo = 0, n = b.seqs;
+  while (n > 1) {
+    const int step = (n + 63) / 64;
+    const int at = lane * step;
+    bool before = false;
+    if (at < n) before = (int64_t)seq_begin(b, lo + at) * mul / div + (int64_t)extra * (lo + at) <= idx;
+    const int hits = max(1, __popcll(__ballot(before)));   // the slots rise with s
+    const int skip = min((hits - 1) * step, n - 1);
+    lo += skip;
+    n = min(step, n - skip);
+  }
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  r.seq = lo;
+  r.t0 = seq_begin(b, lo);
+  r.n = max(0, seq_begin(b, lo + 1) - r.t0);
+  r.len = min(max(b.lens[lo], 0), 1 << 30);
+  r.tile = idx - (int)((int64_t)r.t0 * mul / div) - extra * lo;
+  return r;
+}
+// Tiles of `size` tokens or rows (row = token * group + ...): a sequence of n has at most n / size + extra of them.
+__device__ __forceinline__ SeqTile find_tile(const rq_seq_batch& b, int size, int extra, int idx) {
+  return find_slot(b, 1, size, extra, idx);
+}
+__device__ __forceinline__ SeqTile find_tile_rows(const rq_seq_batch& b, int size, int group, int idx) {
+  return find_slot(b, group, size, 1, idx);
+}
+// The sequence of a token (seq -1: of none).
+__device__ __forceinline__ SeqTile find_token(const rq_seq_batch& b, int t) {
+  SeqTile r = find_slot(b, 1, 1, 0, t);
+  if (r.seq >= 0 && (t < r.t0 || t >= r.t0 + r.n)) r.seq = -1;
+  return r;
+}
+
 // ---------------------------------------------------------------- host side
 
 constexpr int kCUs = 256;                 // MI355X compute units
@@ -229,6 +281,29 @@ size_t dense_tiled_bytes(int64_t rows, int D);
 hipError_t launch_pack_dense(const uint16_t* E, int64_t rows, int D, uint16_t* Et, hipStream_t stream);
 hipError_t launch_dense_logits(const uint16_t* Et, int64_t rows, int D, const float* h, int B, float softcap,
                                float* logits, uint64_t* block_keys, uint16_t* hb, hipStream_t stream);
+
+// 4-bit matrices (q4_matvec.hip).
+size_t q4_codes_bytes(int64_t rows, int D);
+size_t q4_scale_count(int64_t rows, int D, int group);
+hipError_t launch_pack_q4_codes(const uint8_t* src, int64_t rows, int D, void* dst, hipStream_t stream);
+hipError_t launch_pack_q4_scales(const void* src, int64_t rows, int D, int group, int elem_bytes, void* dst, hipStream_t stream);
+// ws: q4_matvec_ws_bytes (0: none), 256-byte aligned.
+size_t q4_matvec_ws_bytes(const rq_q4_matrix* W, int x_dtype, bool x2, int B);
+hipError_t launch_q4_matvec(const rq_q4_matrix* W, const void* x, int x_dtype, const float* x2, int B, float* y, void* ws,
+                            hipStream_t stream);
+// Rotary positions (rope.hip).
+hipError_t launch_rope(const void* x, int x_dtype, int tokens, int heads, int size, int64_t x_stride, const int32_t* positions,
+                       const double* freqs, int rot, int layout, float mscale, int inverse, void* out, int out_dtype,
+                       int64_t out_stride, hipStream_t stream);
+hipError_t launch_rope_append(const rq_seq_batch* batch, const rq_kv_cache* cache, const void* q, const void* k, const void* v,
+                              int in_dtype, int64_t q_stride, int64_t k_stride, int64_t v_stride, int heads,
+                              const int32_t* positions, const double* freqs, int rot, int layout, float mscale, void* q_out,
+                              int32_t* bad, hipStream_t stream);
+// Attention over the paged cache (paged_attn.hip).
+size_t paged_attn_ws_bytes(const rq_kv_cache* c, int tokens, int seqs, int heads, int max_len);
+hipError_t launch_paged_attn(const rq_seq_batch* batch, const rq_kv_cache* cache, const void* q, int64_t q_stride, int heads,
+                             float scale, float softcap, int window, int max_len, void* out, float* lse, int32_t* bad,
+                             void* ws, hipStream_t stream);
 
 constexpr int kEpiRowsPerBlock = 1024;   // rows per epilogue workgroup
 inline int epi_blocks(int64_t rows) { return (int)((rows + kEpiRowsPerBlock - 1) / kEpiRowsPerBlock); }
