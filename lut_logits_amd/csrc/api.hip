@@ -890,6 +890,7 @@ rq_status rq_paged_attn(const rq_seq_batch* batch, const rq_kv_cache* cache, con
   if (s == RQ_OK) s = check_stride("paged_attn: q", q_stride, heads, cache->head_dim);
   if (s != RQ_OK) return s;
   if (window < 0) return fail(RQ_ERR_SHAPE, "window=%d < 0", window);
+  if (!(scale > 0.0f) || !(scale < __builtin_huge_valf())) return fail(RQ_ERR_SHAPE, "scale=%g is not positive and finite", (double)scale);
   if (batch->seqs == 0 || batch->tokens == 0) return RQ_OK;
   if (!q || !out) return fail(RQ_ERR_NULL, "paged_attn: NULL buffer");
   if (q == out) return fail(RQ_ERR_SHAPE, "paged_attn: out must not be q");

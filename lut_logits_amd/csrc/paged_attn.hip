@@ -23,7 +23,7 @@
 //
 // Keys that no row of a tile sees (places past the end, stale pages, before the window) are not multiplied: their V is set to zero
 // bits and their scores to -inf whatever the memory holds. A tile whose visible V holds infinities or NaN and that not all rows see
-// alike goes key by key (careful_pv), so that such a value reaches only the rows that see it.
+// alike is not multiplied as it is: such values are taken out and reach only the rows that see them.
 #include "rq_internal.h"
 
 namespace rq {
@@ -105,6 +105,23 @@ __device__ __forceinline__ int page_of(const AttnArgs& a, const int32_t* table, 
   return (unsigned)p < (unsigned)a.cache.pages ? p : -1;
 }
 
+// 64 entries of a sequence's table, one a lane (-1: no page): one load for many tiles instead of a wait in each.
+struct PageWindow {
+  int first = 0, id = -1;
+  __device__ __forceinline__ void load(const AttnArgs& a, const int32_t* table, int entry) {
+    first = entry;
+    const int i = entry + (int)(threadIdx.x & 63);
+    id = -1;
+    if (i < a.batch.max_pages) {
+      const int p = table[i];
+      if ((unsigned)p < (unsigned)a.cache.pages) id = p;
+    }
+  }
+  __device__ __forceinline__ bool holds(int entry) const { return (unsigned)(entry - first) < 64u; }
+  __device__ __forceinline__ int at(int entry) const { return __builtin_amdgcn_readlane(id, entry - first); }      // entry uniform
+  __device__ __forceinline__ int at_lane(int entry) const { return __shfl(id, entry - first, 64); }                // a lane's own
+};
+
 template <bool F16>
 struct Type {
   typedef bf16x8 vec;
@@ -140,14 +157,14 @@ struct Type<true> {
   static constexpr uint32_t kExp = 0x7c00u;
 };
 
-// Base-2 score of a product q.k. tanh(u) = 1 - 2 / (1 + e^2u): its absolute error of 1e-7 is 1e-5 of a
+// Base-2 score of a product q.k under a cap. tanh(u) = 1 - 2 / (1 + e^2u): its absolute error of 1e-7 is 1e-5 of a
 // probability at a cap of 50, far below the rounding of 16-bit outputs.
+__device__ __forceinline__ float capped(const AttnArgs& a, float z) {
+  const float e = __builtin_amdgcn_exp2f(z * a.cap_in * (2.0f * kLog2e));
+  return a.cap_out * (1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + e));
+}
 __device__ __forceinline__ float score(const AttnArgs& a, float z) {
-  if (a.cap_out > 0.0f) {   // (uniform)
-    const float e = __builtin_amdgcn_exp2f(z * a.cap_in * (2.0f * kLog2e));
-    return a.cap_out * (1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + e));
-  }
-  return z * a.z_scale;
+  return a.cap_out > 0.0f ? capped(a, z) : z * a.z_scale;   // (uniform)
 }
 
 // Whether a word holds an infinity or NaN in either half.
@@ -155,6 +172,42 @@ template <bool F16>
 __device__ __forceinline__ bool not_finite(uint32_t w) {
   constexpr uint32_t m = Type<F16>::kExp;
   return (w & m) == m || (w & (m << 16)) == (m << 16);
+}
+
+// The word with an infinity or NaN in either half replaced by zero bits.
+template <bool F16>
+__device__ __forceinline__ uint32_t finite_halves(uint32_t w) {
+  constexpr uint32_t m = Type<F16>::kExp;
+  return ((w & m) == m ? 0u : w & 0xffffu) | ((w & (m << 16)) == (m << 16) ? 0u : w & 0xffff0000u);
+}
+
+// Adds the infinities and NaN of V that were taken out to the rows that see them, once this workgroup has stored its rows: a
+// thread takes a column and reads its keys again, those that `out` says were treated so. A probability is above zero, so that the
+// product is the value itself.
+template <int DH, bool F16, typename Out>
+__device__ __forceinline__ void add_not_finite(const AttnArgs& a, const RowTile& r, const int32_t* table, int lo, int hi, int kvh,
+                                            int split, Out out) {
+  __threadfence_block();
+  __syncthreads();
+  const int d = threadIdx.x;
+  if (d >= DH) return;
+#pragma unroll 1
+  for (int key = lo; key < hi; ++key) {
+    const int p = page_of(a, table, key);
+    if (p < 0 || !out(key)) continue;
+    const uint16_t bits = static_cast<const uint16_t*>(a.cache.v)[((((int64_t)p * a.cache.kv_heads + kvh) * DH + d) << a.page_shift) +
+                                                                  (key & ((1 << a.page_shift) - 1))];
+    if (!not_finite<F16>(bits)) continue;
+    const float v = Type<F16>::lo(bits);
+#pragma unroll 1
+    for (int i = 0; i < r.rows; ++i) {
+      const int tk = (r.row0 + i) / a.group, at = r.place0 + tk;
+      if (key > at || (a.window > 0 && key <= at - a.window)) continue;
+      const int64_t th = (int64_t)(r.t0 + tk) * a.heads + kvh * a.group + r.row0 + i - tk * a.group;
+      if (a.splits > 1) a.part_o[(th * a.splits + split) * DH + d] += v;
+      else a.out[th * DH + d] = (uint16_t)Type<F16>::round2(Type<F16>::lo(a.out[th * DH + d]) + v, 0.0f);
+    }
+  }
 }
 
 // ---------------------------------------------------------------- few rows
@@ -165,6 +218,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 8))
   constexpr int KS = DH / 32;   // steps of q.k
   constexpr int DT = DH / 16;   // column tiles of V
   __shared__ float2 ml[4][kRowsSmall];
+  __shared__ int wilds[4];
   extern __shared__ __align__(16) float osh[];   // [4][16][DH + 4]
   constexpr int OLD = DH + 4;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -194,11 +248,12 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 8))
 #pragma unroll
   for (int d = 0; d < DT; ++d) o[d] = floatx4{0.f, 0.f, 0.f, 0.f};
   float m = kNegInf, l = 0.0f;
+  bool wild = false;           // (uniform in a wave) V holds infinities or NaN in this wave's tiles
+  int lo = 0, hi = 0;
+  const int32_t* table = a.batch.table + (int64_t)r.seq * a.batch.max_pages;
 
   if (!none) {
-    int lo, hi;
     split_range(r, split, lo, hi);
-    const int32_t* table = a.batch.table + (int64_t)r.seq * a.batch.max_pages;
     // places of the tile's first and last row
     const int place_a = r.place0 + r.row0 / a.group, place_b = r.place0 + (r.row0 + r.rows - 1) / a.group;
     const int64_t page_elems = (int64_t)a.cache.kv_heads << a.page_shift;   // * DH
@@ -208,10 +263,13 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 8))
     const int krow = 8 * (i16 >> 2) + (i16 & 3);   // this lane's key of sub-tile 0 (sub-tile 1: + 4)
     const int t_end = (hi + 31) / 32;
     u32x4 kf[2][KS], vf[DT];
+    PageWindow win;
     // the two halves of a tile of 32 keys may lie in two pages of 16
     auto pages = [&](int t, int& p0, int& p1) {
-      p0 = page_of(a, table, 32 * t);
-      p1 = page_of(a, table, 32 * t + 16);
+      const int e0 = (32 * t) >> a.page_shift, e1 = (32 * t + 16) >> a.page_shift;
+      if (!win.holds(e0) || !win.holds(e1)) win.load(a, table, e0);
+      p0 = win.at(e0);
+      p1 = win.at(e1);
     };
     auto load_k = [&](int t, int p0, int p1) {
       const int p = max(0, krow < 16 ? p0 : p1);
@@ -227,9 +285,13 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 8))
 #pragma unroll
       for (int d = 0; d < DT; ++d) vf[d] = *reinterpret_cast<const u32x4*>(vp + ((int64_t)(16 * d) << a.page_shift));
     };
+    // A second time only where the first left an infinity or NaN: with such values of V taken out (they are added at the end to
+    // the rows that see them).
+    for (int pass = 0; pass < 2; ++pass) {
     int t = lo / 32 + wave;
     int p0 = -1, p1 = -1, n0 = -1, n1 = -1;
     if (t < t_end) {
+      win.load(a, table, (32 * t) >> a.page_shift);
       pages(t, p0, p1);
       load_k(t, p0, p1);
       load_v(t, p0, p1);
@@ -251,20 +313,17 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 8))
       const bool whole = pages_ok && 32 * t >= lo && 32 * t + 31 < hi && 32 * t + 31 <= place_a &&
                          (a.window <= 0 || 32 * t > place_b - a.window);   // every row sees every key
       float z[8];
-      uint32_t seen = 0xffu;
 #pragma unroll
       for (int j = 0; j < 8; ++j) z[j] = score(a, s[j >> 2][j & 3]);
       if (!whole) {   // (uniform)
         const bool ok = (kg < 2 ? p0 : p1) >= 0;
-        seen = 0;
         uint32_t any = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int key = key0 + j;
           const bool in = ok && key >= lo && key < hi;
           if (in) any |= 1u << j;
-          if (in && key <= place && (a.window <= 0 || key > place - a.window)) seen |= 1u << j;
-          if (!(seen >> j & 1)) z[j] = kNegInf;
+          if (!(in && key <= place && (a.window <= 0 || key > place - a.window))) z[j] = kNegInf;
         }
         // V of keys that are no one's: zero bits
         u32x4 keep;
@@ -296,41 +355,14 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 8))
         ph[j] = Ty::round2(x, y);
         pl[j] = Ty::round2(x - Ty::lo(ph[j]), y - Ty::hi(ph[j]));
       }
-      // (also where every row sees every key: an infinity must not meet the zeros of P's low part)
-      bool wild = false;
+      if (pass > 0) {   // (uniform)
 #pragma unroll
-      for (int d = 0; d < DT; ++d)
+        for (int d = 0; d < DT; ++d)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) wild |= not_finite<F16>(vf[d][j]);
-      wild = __any(wild);
-      if (wild) {   // key by key: a row takes only what it sees
-        for (int k = 0; k < 32; ++k) {
-          const uint32_t word = (k & 7) >> 1, half = (k & 1) ? 0xffff0000u : 0xffffu;
-          const bool mine = kg == k >> 3;
-          u32x4 pk, plk, keep;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            keep[j] = mine && (uint32_t)j == word ? half : 0u;
-            pk[j] = ph[j] & keep[j];
-            plk[j] = pl[j] & keep[j];
-          }
-          const bool sees = __shfl((int)(seen >> (k & 7)) & 1, i16 + 16 * (k >> 3), 64);
-#pragma unroll
-          for (int d = 0; d < DT; ++d) {
-            const u32x4 vk = vf[d] & keep;
-            // the low part of P only meets finite values (inf * 0 would be NaN)
-            u32x4 fin;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) fin[j] = not_finite<F16>(vk[j]) ? 0u : vk[j];
-            const floatx4 with = Ty::mfma16(fin, plk, Ty::mfma16(vk, pk, o[d]));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[d][e] = sees ? with[e] : o[d][e];
-          }
-        }
-      } else {
-#pragma unroll
-        for (int d = 0; d < DT; ++d) o[d] = Ty::mfma16(vf[d], pl, Ty::mfma16(vf[d], ph, o[d]));
+          for (int j = 0; j < 4; ++j) vf[d][j] = finite_halves<F16>(vf[d][j]);
       }
+#pragma unroll
+      for (int d = 0; d < DT; ++d) o[d] = Ty::mfma16(vf[d], pl, Ty::mfma16(vf[d], ph, o[d]));
       if (more) {
         load_v(t + 4, n0, n1);
         p0 = n0;
@@ -338,12 +370,25 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 8))
         if (t + 8 < t_end) pages(t + 8, n0, n1);
       }
     }
+    bool found = false;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) found |= (__float_as_uint(o[d][e]) & 0x7f800000u) == 0x7f800000u;
+    if (pass > 0 || !__any(found)) break;
+    wild = true;
+    m = kNegInf;
+    l = 0.0f;
+#pragma unroll
+    for (int d = 0; d < DT; ++d) o[d] = floatx4{0.f, 0.f, 0.f, 0.f};
+    }
     l += __shfl_xor(l, 16, 64);
     l += __shfl_xor(l, 32, 64);
   }
 
   // join the waves: rows' maxima and sums, then the outputs, in wave order
   if (kg == 0) ml[wave][i16] = make_float2(m, l);
+  if (lane == 0) wilds[wave] = wild;
 #pragma unroll
   for (int d = 0; d < DT; ++d) *reinterpret_cast<floatx4*>(osh + ((size_t)wave * 16 + i16) * OLD + 16 * d + 4 * kg) = o[d];
   __syncthreads();
@@ -372,6 +417,8 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 8))
       if (c == 0 && a.lse) a.lse[th] = ll == 0.0f ? kNegInf : (mm + log2f(ll)) * kLn2;
     }
   }
+  if (wilds[0] | wilds[1] | wilds[2] | wilds[3])   // (uniform)
+    add_not_finite<DH, F16>(a, r, table, lo, hi, kvh, split, [&](int key) { return wilds[(key / 32 - lo / 32) & 3] != 0; });
 }
 
 // ---------------------------------------------------------------- many rows
@@ -384,7 +431,7 @@ constexpr int tile_keys() { return DH == 256 ? 32 : 64; }
 __device__ __forceinline__ int key_of_row(int i) { return (i & ~12) | ((i & 4) << 1) | ((i & 8) >> 1); }
 
 template <int DH, bool F16>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))) void attn_tile_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 4))) void attn_tile_kernel(AttnArgs a) {
   typedef Type<F16> Ty;
   constexpr int BK = tile_keys<DH>();
   constexpr int NS = BK / 32;        // key sub-tiles of 32
@@ -426,190 +473,194 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[d][e] = 0.0f;
   float m = kNegInf, l = 0.0f;
+  int wild = 0;                // (uniform) infinities or NaN wait to be added
+  int lo = 0, hi = 0;
+  const int32_t* table = a.batch.table + (int64_t)r.seq * a.batch.max_pages;
 
   if (!none) {
-    int lo, hi;
     split_range(r, split, lo, hi);
-    const int32_t* table = a.batch.table + (int64_t)r.seq * a.batch.max_pages;
     const int place_a = r.place0 + wrow / a.group, place_b = r.place0 + wlast / a.group;
+    const int tile_a = r.place0 + r.row0 / a.group, tile_b = r.place0 + (r.row0 + r.rows - 1) / a.group;   // all waves' rows
     const int64_t page_elems = ((int64_t)a.cache.kv_heads << a.page_shift) * DH;
     const int pmask = (1 << a.page_shift) - 1;
     const uint16_t* kbase = static_cast<const uint16_t*>(a.cache.k) + ((int64_t)kvh << a.page_shift) * DH;
     const uint16_t* vbase = static_cast<const uint16_t*>(a.cache.v) + ((int64_t)kvh << a.page_shift) * DH;
-    auto pages = [&](int t, int (&p)[PG]) {
-#pragma unroll
-      for (int i = 0; i < PG; ++i) p[i] = page_of(a, table, BK * t + 16 * i);
-    };
-    auto page_at = [&](const int (&p)[PG], int off) {   // off: key - BK t
-      int x = p[0];
-#pragma unroll
-      for (int i = 1; i < PG; ++i) x = off >= 16 * i ? p[i] : x;
-      return max(0, x);
-    };
-    // copies tile t into buffer b: 16 bytes a lane, lane after lane in LDS, so the swizzle is in what each lane fetches
-    auto copy = [&](int b, int t, const int (&p)[PG]) {
-      unsigned char* kd = smem + (size_t)b * 2 * CH * 16;
+    PageWindow win;
+    auto entry = [&](int key) { return key >> a.page_shift; };
+    // Copies tile t into buffer b: 16 bytes a lane, lane after lane in LDS, so the swizzle is in what each lane fetches.
+    // Chunk c = 256 j + tid of K is row c / KC: its 16 keys' page is the same for a whole wave, and what depends on the
+    // lane (its key among the 16, its place in the row) does not change with j. A lane's chunk of V keeps its keys
+    // over j, 8 of them, so one page.
+    const int kx = tid / KC;                                    // row, less the part of j
+    const int k_lane = key_of_row(kx & 15) * DH + 8 * ((tid % KC) ^ (kx & 7));
+    const int vx = tid / VC;
+    const int v_keys = 8 * ((tid % VC) ^ (VC == 8 ? (vx & 7) : ((vx >> 1) & 3)));
+    auto copy = [&](int b, int t) {
+      unsigned char* kd = smem + (size_t)b * 2 * CH * 16 + wave * 1024;
       unsigned char* vd = kd + (size_t)CH * 16;
 #pragma unroll
       for (int j = 0; j < CH / kThreads; ++j) {
-        const int c = j * kThreads + tid;
-        const int i = c / KC, ch = (c % KC) ^ (i & 7);
-        const int off = key_of_row(i);
-        const uint16_t* src = kbase + page_at(p, off) * page_elems + (int64_t)((BK * t + off) & pmask) * DH + 8 * ch;
-        __builtin_amdgcn_global_load_lds((const void*)src, (lds_ptr_t)(kd + (size_t)(j * kThreads + wave * 64) * 16), 16, 0, 0);
+        constexpr int kRows = kThreads / KC;                    // rows of 256 chunks: 8, 16 or 32
+        const int i0 = kRows * j + (kRows == 32 ? (wave * 8 & ~15) : 0);
+        const int g = i0 >> 4;                                  // 16 keys (uniform)
+        const int pg = win.at(entry(BK * t + 16 * g));
+        const uint16_t* src = kbase + (int64_t)max(0, pg) * page_elems + (int64_t)(((BK * t + 16 * g) & pmask) + (kRows == 8 ? 4 * (j & 1) : 0)) * DH;
+        __builtin_amdgcn_global_load_lds((const void*)(src + k_lane), (lds_ptr_t)(kd + (size_t)j * kThreads * 16), 16, 0, 0);
       }
+      const int pg = win.at_lane(entry(BK * t + v_keys));
+      const uint16_t* src = vbase + (int64_t)max(0, pg) * page_elems + ((int64_t)vx << a.page_shift) + ((BK * t + v_keys) & pmask);
 #pragma unroll
-      for (int j = 0; j < CH / kThreads; ++j) {
-        const int c = j * kThreads + tid;
-        const int i = c / VC;
-        const int ch = (c % VC) ^ (VC == 8 ? (i & 7) : ((i >> 1) & 3));
-        const uint16_t* src = vbase + page_at(p, 8 * ch) * page_elems + ((int64_t)i << a.page_shift) + ((BK * t + 8 * ch) & pmask);
-        __builtin_amdgcn_global_load_lds((const void*)src, (lds_ptr_t)(vd + (size_t)(j * kThreads + wave * 64) * 16), 16, 0, 0);
+      for (int j = 0; j < CH / kThreads; ++j)
+        __builtin_amdgcn_global_load_lds((const void*)(src + ((int64_t)(kThreads / VC * j) << a.page_shift)),
+                                         (lds_ptr_t)(vd + (size_t)j * kThreads * 16), 16, 0, 0);
+    };
+    // where this lane reads: chunk 2k + h of row i32 of K, chunk 4u + 2g + h of row i32 of V, both swizzled; the even parts of the
+    // chunk numbers are flipped in by the reader
+    const uint32_t k_read = i32 * KC * 16 + ((h ^ (i32 & 7)) << 4);
+    const uint32_t v_read = CH * 16 + i32 * VC * 16 + ((h ^ (VC == 8 ? (i32 & 7) : ((i32 >> 1) & 3))) << 4);
+    const float zs = a.cap_out > 0.0f ? 1.0f : a.z_scale;   // scores enter the exponentials as zs * s - zs * max
+    // One tile from buffer b. whole: every row of the wave sees every key
+    auto attend = [&](int b, int t, bool whole) {
+      const uint32_t kl = k_read + b * (2 * CH * 16), vl = v_read + b * (2 * CH * 16);
+      floatx16 s[NS];
+#pragma unroll
+      for (int u = 0; u < NS; ++u) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[u][e] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const u32x4 kf = *reinterpret_cast<const u32x4*>(smem + (kl ^ ((k & 3) << 5)) + (k >> 2) * 128 + u * 32 * KC * 16);
+          s[u] = Ty::mfma32(kf, qf[k], s[u]);
+        }
       }
+      if (a.cap_out > 0.0f) {   // (uniform)
+#pragma unroll
+        for (int u = 0; u < NS; ++u)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) s[u][e] = capped(a, s[u][e]);
+      }
+      // s[u][8 g + j]: key BK t + 32 u + 16 g + 8 h + j of this lane's row
+      if (!whole) {   // (uniform)
+        // the row's keys: from k_lo on, span more (none: no difference fits)
+        const int k_lo = max(lo, a.window > 0 ? place - a.window + 1 : 0), k_hi = min(hi - 1, place);
+        const uint32_t span = k_hi < k_lo ? 0u : (uint32_t)(k_hi - k_lo);
+        const int first = k_hi < k_lo ? -(1 << 30) : BK * t + 8 * h - k_lo;
+#pragma unroll
+        for (int u = 0; u < NS; ++u)
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const bool page_ok = win.at(entry(BK * t + 32 * u + 16 * g)) >= 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (!page_ok || (uint32_t)(first + 32 * u + 16 * g + j) > span) s[u][8 * g + j] = kNegInf;
+          }
+      }
+      float mt = kNegInf;
+#pragma unroll
+      for (int u = 0; u < NS; ++u)
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) mt = fmaxf(fmaxf(mt, s[u][e]), s[u][e + 1]);
+      mt = fmaxf(mt, __shfl_xor(mt, 32, 64));
+      const float mn = fmaxf(m, mt);
+      const float mu = mn == kNegInf ? 0.0f : mn * zs;
+      if (__any(mn > m)) {   // some row's maximum grew
+        const float f = __builtin_amdgcn_exp2f(mn == kNegInf ? 0.0f : (m - mn) * zs);
+        l *= f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[d] *= f;
+        m = mn;
+      }
+      // One multiply-add a score. The rounding of mu is then a factor common to the row, 2^(|mu| 2^-24) at most; where that is more
+      // than 2^-14, the differences are taken first.
+      float ze = zs, me = mu;
+      if (__any(fabsf(mu) > 1024.0f)) {
+        const float top = mn == kNegInf ? 0.0f : mn;
+#pragma unroll
+        for (int u = 0; u < NS; ++u)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) s[u][e] = (s[u][e] - top) * zs;
+        ze = 1.0f;
+        me = 0.0f;
+      }
+      u32x4 pf[NS][2];
+#pragma unroll
+      for (int u = 0; u < NS; ++u)
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float x = __builtin_amdgcn_exp2f(fmaf(s[u][8 * g + 2 * j], ze, -me));
+            const float y = __builtin_amdgcn_exp2f(fmaf(s[u][8 * g + 2 * j + 1], ze, -me));
+            l += x + y;
+            pf[u][g][j] = Ty::round2(x, y);   // rounded to the cache's type: half a step of each probability
+          }
+      auto v_at = [&](int d, int u, int g) {
+        return *reinterpret_cast<const u32x4*>(smem + (vl ^ ((2 * u + g) << 5)) + d * 32 * VC * 16);
+      };
+#pragma unroll
+      for (int u = 0; u < NS; ++u)
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+          for (int d = 0; d < DT; ++d) o[d] = Ty::mfma32(v_at(d, u, g), pf[u][g], o[d]);
     };
     const int t0 = lo / BK, t_end = (hi + BK - 1) / BK;
-    int p[PG], pn[PG];
-    pages(t0, p);
-    copy(0, t0, p);
-#pragma unroll
-    for (int i = 0; i < PG; ++i) pn[i] = p[i];
-    if (t0 + 1 < t_end) pages(t0 + 1, pn);
+    // the window holds a tile's pages and the next one's
+    auto look = [&](int t) {
+      if (!win.holds(entry(BK * t)) || !win.holds(entry(BK * (t + 2) - 1))) win.load(a, table, entry(BK * t));
+    };
+    win.load(a, table, entry(BK * t0));
+    copy(0, t0);
     for (int t = t0; t < t_end; ++t) {
       const int b = (t - t0) & 1;
       __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): this wave's copies of the tile have landed
       __syncthreads();                      // and everyone's; the other buffer has been read
-      if (t + 1 < t_end) copy(b ^ 1, t + 1, pn);
+      look(t);
+      if (t + 1 < t_end) copy(b ^ 1, t + 1);
+      // The same for the whole workgroup: V of keys that are no one's becomes zero bits; so do infinities and NaN that not all
+      // rows see, which are added to the rows that do at the end (wild)
+      bool ours = BK * t >= lo && BK * t + BK - 1 < hi;
+#pragma unroll
+      for (int i = 0; i < PG; ++i) ours = ours && win.at(entry(BK * t + 16 * i)) >= 0;
+      if (!ours || BK * t + BK - 1 > tile_a || (a.window > 0 && BK * t <= tile_b - a.window)) {
+        bool found = false;
+#pragma unroll
+        for (int j = 0; j < CH / kThreads; ++j) {
+          u32x4* at = reinterpret_cast<u32x4*>(smem + b * (2 * CH * 16) + CH * 16 + (j * kThreads + tid) * 16);
+          u32x4 v = *at;
+          const int pg = win.at_lane(entry(BK * t + v_keys));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int key = BK * t + v_keys + 2 * i;
+            v[i] &= (pg >= 0 && key >= lo && key < hi ? 0xffffu : 0u) | (pg >= 0 && key + 1 >= lo && key + 1 < hi ? 0xffff0000u : 0u);
+            found |= not_finite<F16>(v[i]);
+            v[i] = finite_halves<F16>(v[i]);
+          }
+          *at = v;
+        }
+        wild |= __syncthreads_or(found);
+      }
       const bool hidden = idle || BK * t > place_b || (a.window > 0 && BK * t + BK - 1 <= place_a - a.window);
       if (!hidden) {   // (uniform)
-        const unsigned char* kl = smem + (size_t)b * 2 * CH * 16;
-        const unsigned char* vl = kl + (size_t)CH * 16;
-        bool ok = true;
-#pragma unroll
-        for (int i = 0; i < PG; ++i) ok = ok && p[i] >= 0;
-        const bool whole = ok && BK * t >= lo && BK * t + BK - 1 < hi && BK * t + BK - 1 <= place_a &&
-                           (a.window <= 0 || BK * t > place_b - a.window);
-        floatx16 s[NS];
-#pragma unroll
-        for (int u = 0; u < NS; ++u) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) s[u][e] = 0.0f;
-#pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            const int i = 32 * u + i32;
-            const u32x4 kf = *reinterpret_cast<const u32x4*>(kl + ((size_t)i * KC + ((2 * k + h) ^ (i & 7))) * 16);
-            s[u] = Ty::mfma32(kf, qf[k], s[u]);
-          }
-        }
-        // s[u][8 g + j]: key BK t + 32 u + 16 g + 8 h + j of this lane's row
-        uint32_t seen[NS], any[NS];   // bit 8 g + j
-        float mt = kNegInf;
-#pragma unroll
-        for (int u = 0; u < NS; ++u) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) s[u][e] = score(a, s[u][e]);
-          seen[u] = any[u] = 0xffffu;
-          if (!whole) {   // (uniform)
-            seen[u] = any[u] = 0;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int key = BK * t + 32 * u + 16 * (e >> 3) + 8 * h + (e & 7);
-              const bool in = p[2 * u + (e >> 3)] >= 0 && key >= lo && key < hi;
-              if (in) any[u] |= 1u << e;
-              if (in && key <= place && (a.window <= 0 || key > place - a.window)) seen[u] |= 1u << e;
-              if (!(seen[u] >> e & 1)) s[u][e] = kNegInf;
-            }
-          }
-#pragma unroll
-          for (int e = 0; e < 16; ++e) mt = fmaxf(mt, s[u][e]);
-        }
-        mt = fmaxf(mt, __shfl_xor(mt, 32, 64));
-        const float mn = fmaxf(m, mt);
-        const float mu = mn == kNegInf ? 0.0f : mn;
-        if (__any(mn > m)) {
-          const float f = __builtin_amdgcn_exp2f(m - mu);
-          l *= f;
-#pragma unroll
-          for (int d = 0; d < DT; ++d) o[d] *= f;
-          m = mn;
-        }
-        u32x4 pf[NS][2];
-#pragma unroll
-        for (int u = 0; u < NS; ++u)
-#pragma unroll
-          for (int g = 0; g < 2; ++g)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float x = __builtin_amdgcn_exp2f(s[u][8 * g + 2 * j] - mu), y = __builtin_amdgcn_exp2f(s[u][8 * g + 2 * j + 1] - mu);
-              l += x + y;
-              pf[u][g][j] = Ty::round2(x, y);   // rounded to the cache's type: half a step of each probability
-            }
-        auto v_at = [&](int d, int u, int g) {
-          const int i = 32 * d + i32, ch = 4 * u + 2 * g + h;
-          return *reinterpret_cast<const u32x4*>(vl + ((size_t)i * VC + (ch ^ (VC == 8 ? (i & 7) : ((i >> 1) & 3)))) * 16);
-        };
-        if (whole) {   // (uniform)
-#pragma unroll
-          for (int d = 0; d < DT; ++d)
-#pragma unroll
-            for (int u = 0; u < NS; ++u)
-#pragma unroll
-              for (int g = 0; g < 2; ++g) o[d] = Ty::mfma32(v_at(d, u, g), pf[u][g], o[d]);
-        } else {
-#pragma unroll
-          for (int u = 0; u < NS; ++u)
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              u32x4 keep;   // V of keys that are no one's: zero bits
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                keep[j] = ((any[u] >> (8 * g + 2 * j)) & 1u ? 0xffffu : 0u) | ((any[u] >> (8 * g + 2 * j + 1)) & 1u ? 0xffff0000u : 0u);
-              bool wild = false;
-              u32x4 v[DT];
-#pragma unroll
-              for (int d = 0; d < DT; ++d) {
-                v[d] = v_at(d, u, g) & keep;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) wild |= not_finite<F16>(v[d][j]);
-              }
-              if (!__any(wild)) {
-#pragma unroll
-                for (int d = 0; d < DT; ++d) o[d] = Ty::mfma32(v[d], pf[u][g], o[d]);
-              } else {   // key by key: a row takes only what it sees
-                for (int k = 0; k < 16; ++k) {
-                  u32x4 mine;
-#pragma unroll
-                  for (int j = 0; j < 4; ++j)
-                    mine[j] = h == k >> 3 && j == (k & 7) >> 1 ? ((k & 1) ? 0xffff0000u : 0xffffu) : 0u;
-                  const bool sees = __shfl((int)(seen[u] >> (8 * g + (k & 7))) & 1, i32 + 32 * (k >> 3), 64);
-#pragma unroll
-                  for (int d = 0; d < DT; ++d) {
-                    const floatx16 with = Ty::mfma32(v[d] & mine, pf[u][g] & mine, o[d]);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) o[d][e] = sees ? with[e] : o[d][e];
-                  }
-                }
-              }
-            }
-        }
+        const bool whole = ours && BK * t + BK - 1 <= place_a && (a.window <= 0 || BK * t > place_b - a.window);
+        attend(b, t, whole);
       }
-#pragma unroll
-      for (int i = 0; i < PG; ++i) p[i] = pn[i];
-      if (t + 2 < t_end) pages(t + 2, pn);
     }
     l += __shfl_xor(l, 32, 64);
   }
-  if (idle || 32 * wave + i32 >= r.rows) return;
+  const bool stores = !idle && 32 * wave + i32 < r.rows;
   const int64_t th = (int64_t)(r.t0 + tok) * a.heads + head;
+  const float m2 = a.cap_out > 0.0f ? m : m * a.z_scale;   // the maximum as a base-2 score
   // o[d][e]: column 32 d + 8 (e >> 2) + 4 h + (e & 3)
-  if (a.splits > 1) {   // (uniform)
+  if (stores && a.splits > 1) {
     float* po = a.part_o + (th * a.splits + split) * DH + 4 * h;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
       for (int e = 0; e < 16; e += 4)
         *reinterpret_cast<floatx4*>(po + 32 * d + 2 * e) = floatx4{o[d][e], o[d][e + 1], o[d][e + 2], o[d][e + 3]};
-    if (h == 0) a.part_ml[th * a.splits + split] = make_float2(m, l);
-  } else {
+    if (h == 0) a.part_ml[th * a.splits + split] = make_float2(m2, l);
+  } else if (stores) {
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     uint16_t* op = a.out + th * DH + 4 * h;
 #pragma unroll
@@ -618,8 +669,16 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))
       for (int e = 0; e < 16; e += 4)
         *reinterpret_cast<u32x2*>(op + 32 * d + 2 * e) =
             u32x2{Ty::round2(o[d][e] * inv, o[d][e + 1] * inv), Ty::round2(o[d][e + 2] * inv, o[d][e + 3] * inv)};
-    if (h == 0 && a.lse) a.lse[th] = l == 0.0f ? kNegInf : (m + log2f(l)) * kLn2;
+    if (h == 0 && a.lse) a.lse[th] = l == 0.0f ? kNegInf : (m2 + log2f(l)) * kLn2;
   }
+  if (!wild) return;
+  const int tile_a = r.place0 + r.row0 / a.group, tile_b = r.place0 + (r.row0 + r.rows - 1) / a.group;
+  add_not_finite<DH, F16>(a, r, table, lo, hi, kvh, split, [&](int key) {
+    const int blk = key / BK * BK;
+    bool ours = blk >= lo && blk + BK - 1 < hi;
+    for (int i = 0; i < PG; ++i) ours = ours && page_of(a, table, blk + 16 * i) >= 0;
+    return !(ours && blk + BK - 1 <= tile_a && (a.window <= 0 || blk > tile_b - a.window));
+  });
 }
 
 // ---------------------------------------------------------------- joining the splits
