@@ -1,0 +1,305 @@
+// q4_batch.hip -- products with 4-bit matrices: batches (q4_matvec.hip has the layout, the decoding and few vectors).
+//
+// The activations are cut into their bf16 parts beforehand, once, by a small kernel that lays them out as the
+// matrix core takes them: for each step of 32 columns, part and 16 vectors one block of 1 KB, a lane's 16 bytes in lane order. The
+// parts go into the SAME accumulator, one after the other (their products are exact, so this is one longer fp32 sum), so 16 vectors
+// cost one accumulator tile whatever their type.
+//
+// A wave takes T row blocks: every block of activations that it reads (from L2) meets T decoded blocks of weights. Its loads of codes
+// run one column block ahead, those of activations two or four steps. WK waves of a workgroup split the columns; where the rows are too few to fill the chip, KS workgroups do
+// as well, and their sums, in the workspace, are added by a last kernel in order.
+//
+// Bound: decoding on the vector unit (T * 14 or 24 operations for T * NB * parts matrix instructions a step) beside HBM up to about
+// 32 vectors, the matrix cores behind.
+#include "q4_matvec.h"
+
+namespace rq {
+namespace {
+
+constexpr int kBatchThreads = 512, kBatchWaves = kBatchThreads / 64;
+
+struct BatchArgs : Q4Args {
+  u32x4* xf;                 // [batch tile][KT][4][parts][NB][64]
+  float* xsum;               // [batch tile][KT][4][16 NB]: sums over the steps' columns, with offsets
+  float* part;               // [KS][B][rows], KS > 1
+  int ks, kper;              // column splits over workgroups, column blocks of one
+};
+
+template <int NB, int T, int P, int GPT, bool WIDE, bool LEV>
+__global__ __launch_bounds__(kBatchThreads) __attribute__((amdgpu_waves_per_eu(2, 8))) void q4_batch_kernel(BatchArgs a) {
+  constexpr int STEPS = 4 / GPT;       // steps of 32 columns in a group
+  typedef Q4Decoder<LEV> Dec;
+  extern __shared__ __align__(16) float red[];   // [wr][wk - 1][T * NB * 4][64]
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);   // (uniform)
+  const int i16 = lane & 15, kg = lane >> 4;
+  const int wk = a.wk, wr = kBatchWaves / wk;
+  const int kpart = wave % wk, rpart = wave / wk;
+  const int split = (int)blockIdx.x % a.ks, rg = (int)blockIdx.x / a.ks * wr + rpart;
+  const int tile = blockIdx.y, b0 = tile * 16 * NB;
+  const int k_lo = split * a.kper, k_hi = min(a.KT, k_lo + a.kper);
+  const u32x4* xf = a.xf + (size_t)tile * a.KT * 4 * P * NB * 64 + lane;
+  const float* xsum = a.xsum + (size_t)tile * a.KT * 4 * 16 * NB + 4 * kg;
+  const Dec decode(a.levels);
+
+  struct Stage {
+    u32x4 c[T];
+    Q4Scales<GPT, WIDE> s[T], o[T];
+  };
+  auto load = [&](Stage& st, int kt) {
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      const int64_t blk = (int64_t)min(rg * T + t, a.RT - 1) * a.KT + min(kt, a.KT - 1);
+      st.c[t] = a.codes[blk * 64 + lane];
+      st.s[t].load(a.scales, blk * 16 + i16);
+      if (a.offsets) st.o[t].load(a.offsets, blk * 16 + i16);   // (uniform)
+    }
+  };
+  floatx4 tot[T][NB];
+#pragma unroll
+  for (int t = 0; t < T; ++t)
+#pragma unroll
+    for (int n = 0; n < NB; ++n) tot[t][n] = floatx4{0.f, 0.f, 0.f, 0.f};
+  // activations of the next R steps
+  constexpr int R = P * NB * T <= 12 ? 4 : 2;   // as the registers allow
+  u32x4 x[R][P][NB];
+  auto load_x = [&](u32x4 (&v)[P][NB], int kt, int w) {
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int n = 0; n < NB; ++n) v[p][n] = xf[(((size_t)min(kt, a.KT - 1) * 4 + w) * P + p) * NB * 64 + n * 64];
+  };
+  Stage s0, s1;
+  load(s0, k_lo + kpart);
+#pragma unroll
+  for (int w = 0; w < R; ++w) load_x(x[w], k_lo + kpart, w);
+  for (int kt = k_lo + kpart; kt < k_hi; kt += wk) {
+    if (kt + wk < k_hi) load(s1, kt + wk);   // (uniform)
+#pragma unroll
+    for (int g = 0; g < GPT; ++g) {
+      floatx4 acc[T][NB];
+#pragma unroll
+      for (int t = 0; t < T; ++t)
+#pragma unroll
+        for (int n = 0; n < NB; ++n) acc[t][n] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = g * STEPS; w < (g + 1) * STEPS; ++w) {
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+          const bf16x8 wv = decode(s0.c[t][w]);
+#pragma unroll
+          for (int p = P - 1; p >= 0; --p)   // the smallest parts first
+#pragma unroll
+            for (int n = 0; n < NB; ++n) acc[t][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[w % R][p][n]), wv, acc[t][n], 0, 0, 0);
+        }
+        if (w + R < 4 || kt + wk < k_hi) load_x(x[w % R], w + R < 4 ? kt : kt + wk, (w + R) % 4);   // the step that this buffer serves next
+      }
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        const float s = s0.s[t].get(g, a.scale_dtype);
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) tot[t][n][e] = fmaf(s, acc[t][n][e], tot[t][n][e]);
+      }
+      if (a.offsets) {   // (uniform)
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          floatx4 xv = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int w = g * STEPS; w < (g + 1) * STEPS; ++w) xv += *reinterpret_cast<const floatx4*>(xsum + ((size_t)kt * 4 + w) * 16 * NB + 16 * n);
+          xv *= 1.0f / Dec::kUnit;
+#pragma unroll
+          for (int t = 0; t < T; ++t) {
+            const float o = s0.o[t].get(g, a.scale_dtype);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) tot[t][n][e] = fmaf(o, xv[e], tot[t][n][e]);
+          }
+        }
+      }
+    }
+    s0 = s1;
+  }
+  if (wk > 1) {   // (uniform) sums of the waves of a row group, in wave order
+    float* r = red + (size_t)rpart * (wk - 1) * (T * NB * 4) * 64 + lane;
+    if (kpart > 0) {
+#pragma unroll
+      for (int t = 0; t < T; ++t)
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) r[(((size_t)(kpart - 1) * T + t) * NB + n) * 256 + e * 64] = tot[t][n][e];
+    }
+    __syncthreads();
+    if (kpart > 0) return;
+    for (int p = 0; p + 1 < wk; ++p)
+#pragma unroll
+      for (int t = 0; t < T; ++t)
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) tot[t][n][e] += r[(((size_t)p * T + t) * NB + n) * 256 + e * 64];
+  }
+  float* y = a.ks > 1 ? a.part + (size_t)split * a.B * a.rows : a.y;
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    const int64_t r = ((int64_t)rg * T + t) * 16 + i16;
+    if (r >= a.rows) continue;
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int b = b0 + 16 * n + 4 * kg + e;
+        if (b < a.B) y[(int64_t)b * a.rows + r] = tot[t][n][e] * Dec::kUnit;
+      }
+  }
+}
+
+// The parts of 8 columns of one vector a thread, a wave for 16 vectors and 32 columns; their sum over the 32.
+template <int SRC>
+__global__ __launch_bounds__(256) void q4_cut_kernel(BatchArgs a, int nb) {
+  const int lane = threadIdx.x & 63, i16 = lane & 15, kg = lane >> 4;
+  const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);   // (batch tile, step, 16 vectors)
+  const int n = (int)(unit % nb);
+  const int64_t step = unit / nb;                                      // tile * KT * 4 + step of 32 columns
+  const int tile = (int)(step / (a.KT * 4)), k0 = (int)(step - (int64_t)tile * a.KT * 4) * 32 + 8 * kg;
+  const int b = (tile * nb + n) * 16 + i16;
+  if (unit >= (int64_t)((a.B + 16 * nb - 1) / (16 * nb)) * a.KT * 4 * nb) return;
+  float v[8], s = 0.0f;
+  Q4Acts<SRC, 8> w;
+  w.load(a, min(b, a.B - 1), k0);
+  w.values(a, k0, v);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    v[j] = b < a.B ? v[j] : 0.0f;
+    s += v[j];
+  }
+  if (a.offsets) {   // (uniform)
+    s += __shfl_xor(s, 16, 64);
+    s += __shfl_xor(s, 32, 64);
+    if (kg == 0) a.xsum[step * 16 * nb + n * 16 + i16] = s;
+  }
+#pragma unroll
+  for (int p = 0; p < q4_parts(SRC); ++p) {
+    uint32_t u[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) u[j] = cut_bf16(v[j]);
+    a.xf[((step * q4_parts(SRC) + p) * nb + n) * 64 + lane] =
+        u32x4{u[0] | (u[1] << 16), u[2] | (u[3] << 16), u[4] | (u[5] << 16), u[6] | (u[7] << 16)};
+  }
+}
+
+__global__ __launch_bounds__(256) void q4_add_kernel(const float* __restrict__ part, int ks, int64_t n, float* __restrict__ y) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n) return;
+  float s = part[i];
+  for (int z = 1; z < ks; ++z) s += part[z * n + i];
+  y[i] = s;
+}
+
+struct BatchPlan {
+  int NB, T;
+  unsigned gx, gy;
+  size_t lds, xf, xsum, part;   // LDS; bytes of the workspace's parts
+};
+
+BatchPlan plan_batch(BatchArgs& a) {
+  BatchPlan p;
+  const int tiles = (a.B + 15) / 16, parts = q4_parts(a.src);
+  p.NB = tiles <= 1 ? 1 : tiles == 2 ? 2 : 4;
+  p.T = p.NB == 4 && parts > 1 ? 2 : 4;
+  p.gy = (unsigned)((tiles + p.NB - 1) / p.NB);
+  a.RG = (a.RT + p.T - 1) / p.T;
+  // Waves of a row group and splits over workgroups by their cost in clocks: a wave's steps (decoding and matrix products
+  // overlap in part), for as many waves as share a SIMD; the activations' way from L2 at 64 bytes a clock and CU; and a further
+  // kernel for the sums, about 2.5 us.
+  double best = 1e30;
+  for (int wk = 1; wk <= kBatchWaves && wk <= a.KT; wk *= 2) {
+    for (int ks = 1; ks <= (a.KT + wk - 1) / wk; ++ks) {
+      const int kper = (a.KT + ks - 1) / ks, rounds = (kper + wk - 1) / wk;
+      if ((a.KT + kper - 1) / kper != ks) continue;
+      const int wr = kBatchWaves / wk;
+      const double wgs = (double)((a.RG + wr - 1) / wr) * p.gy * ks, waves = wgs * kBatchWaves;
+      const double step = 3.0 * p.T * (56 + 16 * parts * p.NB);
+      const double simd = rounds * step * std::max(1.0, waves / (4.0 * kCUs));
+      const double l2 = std::max(1.0, wgs / kCUs) * wr * kper * 4.0 * parts * p.NB * 16;
+      const double cost = std::max(simd, l2) + (ks > 1 ? 6000 : 0);
+      if (cost < best) {
+        best = cost;
+        a.wk = wk;
+        a.ks = ks;
+        a.kper = kper;
+      }
+    }
+  }
+  const int wr = kBatchWaves / a.wk;
+  p.gx = (unsigned)((((int64_t)a.RG + wr - 1) / wr) * a.ks);
+  p.lds = (size_t)wr * (a.wk - 1) * p.T * p.NB * 1024;
+  p.xf = (size_t)p.gy * a.KT * 4 * parts * p.NB * 1024;
+  p.xsum = a.offsets ? (size_t)p.gy * a.KT * 4 * 16 * p.NB * sizeof(float) : 0;   // a multiple of 256
+  p.part = a.ks > 1 ? (size_t)a.ks * a.B * a.rows * sizeof(float) : 0;
+  return p;
+}
+
+template <int NB, int T, int P, int GPT, bool WIDE, bool LEV>
+hipError_t launch_one(const BatchArgs& a, const BatchPlan& p, hipStream_t stream) {
+  hipLaunchKernelGGL((q4_batch_kernel<NB, T, P, GPT, WIDE, LEV>), dim3(p.gx, p.gy), dim3(kBatchThreads), p.lds, stream, a);
+  return hipGetLastError();
+}
+template <int P, int GPT, bool WIDE, bool LEV>
+hipError_t launch_nb(const BatchArgs& a, const BatchPlan& p, hipStream_t stream) {
+  return p.NB == 1   ? launch_one<1, 4, P, GPT, WIDE, LEV>(a, p, stream)
+         : p.NB == 2 ? launch_one<2, 4, P, GPT, WIDE, LEV>(a, p, stream)
+                     : launch_one<4, P == 1 ? 4 : 2, P, GPT, WIDE, LEV>(a, p, stream);
+}
+template <int GPT, bool WIDE, bool LEV>
+hipError_t launch_p(const BatchArgs& a, const BatchPlan& p, hipStream_t stream) {
+  const int parts = q4_parts(a.src);
+  return parts == 1   ? launch_nb<1, GPT, WIDE, LEV>(a, p, stream)
+         : parts == 2 ? launch_nb<2, GPT, WIDE, LEV>(a, p, stream)
+                      : launch_nb<3, GPT, WIDE, LEV>(a, p, stream);
+}
+template <int GPT>
+hipError_t launch_gpt(const BatchArgs& a, const BatchPlan& p, hipStream_t stream) {
+  if (a.scale_dtype == RQ_F32) return a.levels ? launch_p<GPT, true, true>(a, p, stream) : launch_p<GPT, true, false>(a, p, stream);
+  return a.levels ? launch_p<GPT, false, true>(a, p, stream) : launch_p<GPT, false, false>(a, p, stream);
+}
+template <int SRC>
+void launch_cut(const BatchArgs& a, const BatchPlan& p, hipStream_t stream) {
+  const int64_t units = (int64_t)p.gy * a.KT * 4 * p.NB;
+  hipLaunchKernelGGL(q4_cut_kernel<SRC>, dim3((unsigned)((units + 3) / 4)), dim3(256), 0, stream, a, p.NB);
+}
+
+}  // namespace
+
+size_t q4_batch_ws_bytes(Q4Args q, int gpt) {
+  BatchArgs a = {};
+  static_cast<Q4Args&>(a) = q;
+  const BatchPlan p = plan_batch(a);
+  return p.xf + p.xsum + p.part;
+}
+
+hipError_t launch_q4_batch(Q4Args q, int gpt, void* ws, hipStream_t stream) {
+  BatchArgs a = {};
+  static_cast<Q4Args&>(a) = q;
+  const BatchPlan p = plan_batch(a);
+  char* w = static_cast<char*>(ws);
+  a.xf = reinterpret_cast<u32x4*>(w);
+  a.xsum = reinterpret_cast<float*>(w + p.xf);
+  a.part = reinterpret_cast<float*>(w + p.xf + p.xsum);
+  switch (a.src) {
+    case kQ4F32: launch_cut<kQ4F32>(a, p, stream); break;
+    case kQ4Gelu: launch_cut<kQ4Gelu>(a, p, stream); break;
+    case kQ4BF16: launch_cut<kQ4BF16>(a, p, stream); break;
+    default: launch_cut<kQ4F16>(a, p, stream);
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  e = gpt == 4 ? launch_gpt<4>(a, p, stream) : gpt == 2 ? launch_gpt<2>(a, p, stream) : launch_gpt<1>(a, p, stream);
+  if (e != hipSuccess || a.ks == 1) return e;
+  const int64_t n = (int64_t)a.B * a.rows;
+  hipLaunchKernelGGL(q4_add_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream, a.part, a.ks, n, a.y);
+  return hipGetLastError();
+}
+
+}  // namespace rq
