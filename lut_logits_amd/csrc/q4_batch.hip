@@ -13,6 +13,8 @@
 // 32 vectors, the matrix cores behind.
 #include "q4_matvec.h"
 
+#include <cmath>
+
 namespace rq {
 namespace {
 
@@ -20,7 +22,7 @@ constexpr int kBatchThreads = 512, kBatchWaves = kBatchThreads / 64;
 
 struct BatchArgs : Q4Args {
   u32x4* xf;                 // [batch tile][KT][4][parts][NB][64]
-  float* xsum;               // [batch tile][KT][4][16 NB]: sums over the steps' columns, with offsets
+  float* xsum;               // [batch tile][KT * GPT][16 NB]: sums over the groups' columns, with offsets
   float* part;               // [KS][B][rows], KS > 1
   int ks, kper;              // column splits over workgroups, column blocks of one
 };
@@ -29,7 +31,7 @@ template <int NB, int T, int P, int GPT, bool WIDE, bool LEV>
 __global__ __launch_bounds__(kBatchThreads) __attribute__((amdgpu_waves_per_eu(2, 8))) void q4_batch_kernel(BatchArgs a) {
   constexpr int STEPS = 4 / GPT;       // steps of 32 columns in a group
   typedef Q4Decoder<LEV> Dec;
-  extern __shared__ __align__(16) float red[];   // [wr][wk - 1][T * NB * 4][64]
+  extern __shared__ __align__(16) float red[];   // [wr][wk][T * NB * 4][64], then the group sums of this split [kper * GPT][16 NB]
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);   // (uniform)
   const int i16 = lane & 15, kg = lane >> 4;
@@ -39,7 +41,7 @@ __global__ __launch_bounds__(kBatchThreads) __attribute__((amdgpu_waves_per_eu(2
   const int tile = blockIdx.y, b0 = tile * 16 * NB;
   const int k_lo = split * a.kper, k_hi = min(a.KT, k_lo + a.kper);
   const u32x4* xf = a.xf + (size_t)tile * a.KT * 4 * P * NB * 64 + lane;
-  const float* xsum = a.xsum + (size_t)tile * a.KT * 4 * 16 * NB + 4 * kg;
+  float* xs = red + (wk > 1 ? kBatchWaves * T * NB * 256 : 0);
   const Dec decode(a.levels);
 
   struct Stage {
@@ -73,6 +75,11 @@ __global__ __launch_bounds__(kBatchThreads) __attribute__((amdgpu_waves_per_eu(2
   load(s0, k_lo + kpart);
 #pragma unroll
   for (int w = 0; w < R; ++w) load_x(x[w], k_lo + kpart, w);
+  if (a.offsets) {   // (uniform) the group sums, in the decoder's unit
+    const float* from = a.xsum + ((size_t)tile * a.KT + k_lo) * GPT * 16 * NB;
+    for (int i = tid; i < (k_hi - k_lo) * GPT * 16 * NB; i += kBatchThreads) xs[i] = from[i] * (1.0f / Dec::kUnit);
+    __syncthreads();
+  }
   for (int kt = k_lo + kpart; kt < k_hi; kt += wk) {
     if (kt + wk < k_hi) load(s1, kt + wk);   // (uniform)
 #pragma unroll
@@ -105,10 +112,7 @@ __global__ __launch_bounds__(kBatchThreads) __attribute__((amdgpu_waves_per_eu(2
       if (a.offsets) {   // (uniform)
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
-          floatx4 xv = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int w = g * STEPS; w < (g + 1) * STEPS; ++w) xv += *reinterpret_cast<const floatx4*>(xsum + ((size_t)kt * 4 + w) * 16 * NB + 16 * n);
-          xv *= 1.0f / Dec::kUnit;
+          const floatx4 xv = *reinterpret_cast<const floatx4*>(xs + ((kt - k_lo) * GPT + g) * 16 * NB + 16 * n + 4 * kg);
 #pragma unroll
           for (int t = 0; t < T; ++t) {
             const float o = s0.o[t].get(g, a.scale_dtype);
@@ -120,72 +124,76 @@ __global__ __launch_bounds__(kBatchThreads) __attribute__((amdgpu_waves_per_eu(2
     }
     s0 = s1;
   }
-  if (wk > 1) {   // (uniform) sums of the waves of a row group, in wave order
-    float* r = red + (size_t)rpart * (wk - 1) * (T * NB * 4) * 64 + lane;
-    if (kpart > 0) {
-#pragma unroll
-      for (int t = 0; t < T; ++t)
-#pragma unroll
-        for (int n = 0; n < NB; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) r[(((size_t)(kpart - 1) * T + t) * NB + n) * 256 + e * 64] = tot[t][n][e];
-    }
-    __syncthreads();
-    if (kpart > 0) return;
-    for (int p = 0; p + 1 < wk; ++p)
-#pragma unroll
-      for (int t = 0; t < T; ++t)
-#pragma unroll
-        for (int n = 0; n < NB; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) tot[t][n][e] += r[(((size_t)p * T + t) * NB + n) * 256 + e * 64];
-  }
   float* y = a.ks > 1 ? a.part + (size_t)split * a.B * a.rows : a.y;
-#pragma unroll
-  for (int t = 0; t < T; ++t) {
+  auto put = [&](int t, int n, int e, float v) {
     const int64_t r = ((int64_t)rg * T + t) * 16 + i16;
-    if (r >= a.rows) continue;
+    const int b = b0 + 16 * n + 4 * kg + e;
+    if (r < a.rows && b < a.B) y[(int64_t)b * a.rows + r] = v * Dec::kUnit;
+  };
+  if (wk == 1) {   // (uniform)
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) put(t, n, e, tot[t][n][e]);
+    return;
+  }
+  // sums of the waves of a row group in wave order, each wave a share of the result tiles
+  float* r = red + (size_t)rpart * wk * (T * NB * 4) * 64 + lane;
+#pragma unroll
+  for (int t = 0; t < T; ++t)
 #pragma unroll
     for (int n = 0; n < NB; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int b = b0 + 16 * n + 4 * kg + e;
-        if (b < a.B) y[(int64_t)b * a.rows + r] = tot[t][n][e] * Dec::kUnit;
-      }
+      for (int e = 0; e < 4; ++e) r[(((size_t)kpart * T + t) * NB + n) * 256 + e * 64] = tot[t][n][e];
+  __syncthreads();
+  for (int i = kpart; i < T * NB * 4; i += wk) {
+    float v = r[i * 64];
+    for (int p = 1; p < wk; ++p) v += r[(size_t)p * (T * NB * 256) + i * 64];
+    put(i / (4 * NB), i / 4 % NB, i % 4, v);
   }
 }
 
-// The parts of 8 columns of one vector a thread, a wave for 16 vectors and 32 columns; their sum over the 32.
+// A workgroup for 16 vectors and a column block, a wave for one of its steps: the parts of 8 columns of one vector a thread, and the
+// sums over the groups.
 template <int SRC>
-__global__ __launch_bounds__(256) void q4_cut_kernel(BatchArgs a, int nb) {
-  const int lane = threadIdx.x & 63, i16 = lane & 15, kg = lane >> 4;
-  const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);   // (batch tile, step, 16 vectors)
-  const int n = (int)(unit % nb);
-  const int64_t step = unit / nb;                                      // tile * KT * 4 + step of 32 columns
-  const int tile = (int)(step / (a.KT * 4)), k0 = (int)(step - (int64_t)tile * a.KT * 4) * 32 + 8 * kg;
-  const int b = (tile * nb + n) * 16 + i16;
-  if (unit >= (int64_t)((a.B + 16 * nb - 1) / (16 * nb)) * a.KT * 4 * nb) return;
-  float v[8], s = 0.0f;
+__global__ __launch_bounds__(256) void q4_cut_kernel(BatchArgs a, int nb, int gpt) {
+  constexpr int P = q4_parts(SRC);
+  __shared__ float sums[4][16];
+  const int lane = threadIdx.x & 63, step = threadIdx.x >> 6, i16 = lane & 15, kg = lane >> 4;
+  const int n = (int)blockIdx.x % nb;
+  const int blk = (int)blockIdx.x / nb;   // batch tile * KT + column block
+  const int tile = blk / a.KT;
+  const int b = (tile * nb + n) * 16 + i16, k0 = (blk - tile * a.KT) * 128 + 32 * step + 8 * kg;
   Q4Acts<SRC, 8> w;
   w.load(a, min(b, a.B - 1), k0);
+  float v[8], s = 0.0f;
   w.values(a, k0, v);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     v[j] = b < a.B ? v[j] : 0.0f;
     s += v[j];
   }
-  if (a.offsets) {   // (uniform)
-    s += __shfl_xor(s, 16, 64);
-    s += __shfl_xor(s, 32, 64);
-    if (kg == 0) a.xsum[step * 16 * nb + n * 16 + i16] = s;
-  }
 #pragma unroll
-  for (int p = 0; p < q4_parts(SRC); ++p) {
+  for (int p = 0; p < P; ++p) {
     uint32_t u[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) u[j] = cut_bf16(v[j]);
-    a.xf[((step * q4_parts(SRC) + p) * nb + n) * 64 + lane] =
+    a.xf[((((int64_t)blk * 4 + step) * P + p) * nb + n) * 64 + lane] =
         u32x4{u[0] | (u[1] << 16), u[2] | (u[3] << 16), u[4] | (u[5] << 16), u[6] | (u[7] << 16)};
+  }
+  if (!a.offsets) return;   // (uniform)
+  s += __shfl_xor(s, 16, 64);
+  s += __shfl_xor(s, 32, 64);
+  if (kg == 0) sums[step][i16] = s;
+  __syncthreads();
+  const int g = threadIdx.x >> 4;
+  if (g < gpt) {
+    const int steps = 4 / gpt;
+    float t = 0.0f;
+    for (int i = 0; i < steps; ++i) t += sums[g * steps + i][i16];
+    a.xsum[((int64_t)blk * gpt + g) * 16 * nb + n * 16 + i16] = t;
   }
 }
 
@@ -203,54 +211,58 @@ struct BatchPlan {
   size_t lds, xf, xsum, part;   // LDS; bytes of the workspace's parts
 };
 
-BatchPlan plan_batch(BatchArgs& a) {
+BatchPlan plan_batch(BatchArgs& a, int gpt) {
   BatchPlan p;
   const int tiles = (a.B + 15) / 16, parts = q4_parts(a.src);
   p.NB = tiles <= 1 ? 1 : tiles == 2 ? 2 : 4;
-  p.T = p.NB == 4 && parts > 1 ? 2 : 4;
   p.gy = (unsigned)((tiles + p.NB - 1) / p.NB);
-  a.RG = (a.RT + p.T - 1) / p.T;
-  // Waves of a row group and splits over workgroups by their cost in clocks: a wave's steps (decoding and matrix products
-  // overlap in part), for as many waves as share a SIMD; the activations' way from L2 at 64 bytes a clock and CU; and a further
-  // kernel for the sums, about 2.5 us.
+  // Row blocks of a wave, waves of a row group and splits over workgroups, by their cost in clocks. A wave's column block
+  // decodes T blocks (56 or 96 clocks a step) beside their matrix products (16 clocks each); two waves share a SIMD; the activations
+  // come from L2 at 64 bytes a clock and CU; a further kernel for the sums costs about 2.5 us and its bytes. Measured on 2304 x 9216 with
+  // 16 fp32 vectors and 5003 x 2311 with 61 of bf16, the figures with the kernel.
   double best = 1e30;
-  for (int wk = 1; wk <= kBatchWaves && wk <= a.KT; wk *= 2) {
-    for (int ks = 1; ks <= (a.KT + wk - 1) / wk; ++ks) {
-      const int kper = (a.KT + ks - 1) / ks, rounds = (kper + wk - 1) / wk;
-      if ((a.KT + kper - 1) / kper != ks) continue;
-      const int wr = kBatchWaves / wk;
-      const double wgs = (double)((a.RG + wr - 1) / wr) * p.gy * ks, waves = wgs * kBatchWaves;
-      const double step = 3.0 * p.T * (56 + 16 * parts * p.NB);
-      const double simd = rounds * step * std::max(1.0, waves / (4.0 * kCUs));
-      const double l2 = std::max(1.0, wgs / kCUs) * wr * kper * 4.0 * parts * p.NB * 16;
-      const double cost = std::max(simd, l2) + (ks > 1 ? 6000 : 0);
-      if (cost < best) {
-        best = cost;
-        a.wk = wk;
-        a.ks = ks;
-        a.kper = kper;
+  for (int T = 2; T <= (p.NB == 1 ? 4 : 2); T *= 2)
+    for (int wk = 1; wk <= kBatchWaves && wk <= a.KT; wk *= 2)
+      for (int ks = 1; ks <= (a.KT + wk - 1) / wk; ++ks) {
+        const int kper = (a.KT + ks - 1) / ks, wr = kBatchWaves / wk;
+        if ((a.KT + kper - 1) / kper != ks || (a.offsets && kper * gpt * p.NB > 1024)) continue;   // (64 KB of group sums)
+        const double cus = std::ceil((double)(((a.RT + T - 1) / T + wr - 1) / wr) * p.gy * ks / kCUs);   // workgroups of a CU
+        const double decode = T * 4 * (a.levels ? 96 : 56), product = T * 4 * 16.0 * parts * p.NB;
+        const double simd = (kper + wk - 1) / wk * (std::max(decode, product) + 0.35 * std::min(decode, product)) * 2 * cus;
+        const double l2 = cus * wr * kper * 4.0 * parts * p.NB * 16;
+        const double cost = std::max(simd, l2) + (ks > 1 ? 6000 + 8.0 * ks * a.B * a.rows / 1700 : 0);
+        if (cost < best) {
+          best = cost;
+          p.T = T;
+          a.wk = wk;
+          a.ks = ks;
+          a.kper = kper;
+        }
       }
-    }
-  }
+  a.RG = (a.RT + p.T - 1) / p.T;
   const int wr = kBatchWaves / a.wk;
   p.gx = (unsigned)((((int64_t)a.RG + wr - 1) / wr) * a.ks);
-  p.lds = (size_t)wr * (a.wk - 1) * p.T * p.NB * 1024;
+  p.lds = (a.wk > 1 ? (size_t)kBatchWaves * p.T * p.NB * 1024 : 0) + (a.offsets ? (size_t)a.kper * gpt * p.NB * 64 : 0);
   p.xf = (size_t)p.gy * a.KT * 4 * parts * p.NB * 1024;
-  p.xsum = a.offsets ? (size_t)p.gy * a.KT * 4 * 16 * p.NB * sizeof(float) : 0;   // a multiple of 256
+  p.xsum = a.offsets ? ((size_t)p.gy * a.KT * gpt * 16 * p.NB * sizeof(float) + 255) & ~(size_t)255 : 0;
   p.part = a.ks > 1 ? (size_t)a.ks * a.B * a.rows * sizeof(float) : 0;
   return p;
 }
 
 template <int NB, int T, int P, int GPT, bool WIDE, bool LEV>
 hipError_t launch_one(const BatchArgs& a, const BatchPlan& p, hipStream_t stream) {
-  hipLaunchKernelGGL((q4_batch_kernel<NB, T, P, GPT, WIDE, LEV>), dim3(p.gx, p.gy), dim3(kBatchThreads), p.lds, stream, a);
+  auto kern = q4_batch_kernel<NB, T, P, GPT, WIDE, LEV>;
+  if (p.lds > 64 * 1024) {
+    hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)p.lds);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(kern, dim3(p.gx, p.gy), dim3(kBatchThreads), p.lds, stream, a);
   return hipGetLastError();
 }
 template <int P, int GPT, bool WIDE, bool LEV>
 hipError_t launch_nb(const BatchArgs& a, const BatchPlan& p, hipStream_t stream) {
-  return p.NB == 1   ? launch_one<1, 4, P, GPT, WIDE, LEV>(a, p, stream)
-         : p.NB == 2 ? launch_one<2, 4, P, GPT, WIDE, LEV>(a, p, stream)
-                     : launch_one<4, P == 1 ? 4 : 2, P, GPT, WIDE, LEV>(a, p, stream);
+  if (p.NB == 1) return p.T == 4 ? launch_one<1, 4, P, GPT, WIDE, LEV>(a, p, stream) : launch_one<1, 2, P, GPT, WIDE, LEV>(a, p, stream);
+  return p.NB == 2 ? launch_one<2, 2, P, GPT, WIDE, LEV>(a, p, stream) : launch_one<4, 2, P, GPT, WIDE, LEV>(a, p, stream);
 }
 template <int GPT, bool WIDE, bool LEV>
 hipError_t launch_p(const BatchArgs& a, const BatchPlan& p, hipStream_t stream) {
@@ -265,9 +277,8 @@ hipError_t launch_gpt(const BatchArgs& a, const BatchPlan& p, hipStream_t stream
   return a.levels ? launch_p<GPT, false, true>(a, p, stream) : launch_p<GPT, false, false>(a, p, stream);
 }
 template <int SRC>
-void launch_cut(const BatchArgs& a, const BatchPlan& p, hipStream_t stream) {
-  const int64_t units = (int64_t)p.gy * a.KT * 4 * p.NB;
-  hipLaunchKernelGGL(q4_cut_kernel<SRC>, dim3((unsigned)((units + 3) / 4)), dim3(256), 0, stream, a, p.NB);
+void launch_cut(const BatchArgs& a, const BatchPlan& p, int gpt, hipStream_t stream) {
+  hipLaunchKernelGGL(q4_cut_kernel<SRC>, dim3((unsigned)((int64_t)p.gy * a.KT * p.NB)), dim3(256), 0, stream, a, p.NB, gpt);
 }
 
 }  // namespace
@@ -275,23 +286,23 @@ void launch_cut(const BatchArgs& a, const BatchPlan& p, hipStream_t stream) {
 size_t q4_batch_ws_bytes(Q4Args q, int gpt) {
   BatchArgs a = {};
   static_cast<Q4Args&>(a) = q;
-  const BatchPlan p = plan_batch(a);
+  const BatchPlan p = plan_batch(a, gpt);
   return p.xf + p.xsum + p.part;
 }
 
 hipError_t launch_q4_batch(Q4Args q, int gpt, void* ws, hipStream_t stream) {
   BatchArgs a = {};
   static_cast<Q4Args&>(a) = q;
-  const BatchPlan p = plan_batch(a);
+  const BatchPlan p = plan_batch(a, gpt);
   char* w = static_cast<char*>(ws);
   a.xf = reinterpret_cast<u32x4*>(w);
   a.xsum = reinterpret_cast<float*>(w + p.xf);
   a.part = reinterpret_cast<float*>(w + p.xf + p.xsum);
   switch (a.src) {
-    case kQ4F32: launch_cut<kQ4F32>(a, p, stream); break;
-    case kQ4Gelu: launch_cut<kQ4Gelu>(a, p, stream); break;
-    case kQ4BF16: launch_cut<kQ4BF16>(a, p, stream); break;
-    default: launch_cut<kQ4F16>(a, p, stream);
+    case kQ4F32: launch_cut<kQ4F32>(a, p, gpt, stream); break;
+    case kQ4Gelu: launch_cut<kQ4Gelu>(a, p, gpt, stream); break;
+    case kQ4BF16: launch_cut<kQ4BF16>(a, p, gpt, stream); break;
+    default: launch_cut<kQ4F16>(a, p, gpt, stream);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
