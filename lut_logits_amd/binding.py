@@ -547,13 +547,41 @@ def _one_device(**tensors):
     return first
 
 
+def _same_device(names, *tensors):
+    """_one_device for the calls that a decode step makes by the hundred: names (one string) are looked at only on failure."""
+    dev = -1
+    for t in tensors:
+        if t is not None:
+            d = t.get_device()
+            if d != dev:
+                if dev >= 0 or d < 0:
+                    return _one_device(**dict(zip(names.split(), tensors)))
+                dev = d
+    return dev
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _call(fn, dev, *args):
     """fn(*args, stream) on device dev's current stream, with that device current for the launch."""
     if torch.cuda.current_device() == dev:
-        check(fn(*args, _stream()))
+        status = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            check(fn(*args, _stream()))
+            status = fn(*args, _raw_stream(dev))
+    if status != RQ_OK:
+        check(status)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _tensor(t, name, dtype, shape):
+    """_arg of an exact shape, quick where nothing is wrong."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
+        _arg(t, name, dtype, shape=shape)
 
 
 def _typed(t, name, types=tuple(_TYPES)):
@@ -567,6 +595,10 @@ def _typed(t, name, types=tuple(_TYPES)):
 def _heads_arg(t, name, heads=None, size=None, tokens=None, dtype=None):
     """A [tokens][heads][size] tensor whose heads lie one behind the other; tokens may be further apart (a
     view of a stacked projection). Returns the token stride in elements."""
+    if isinstance(t, torch.Tensor) and t.dim() == 3 and t.is_contiguous() and (t.dtype in _TYPES if dtype is None else t.dtype is dtype):
+        T, h, n = t.shape
+        if (heads is None or h == heads) and (size is None or n == size) and (tokens is None or T == tokens):
+            return h * n
     _typed(t, name, tuple(_TYPES) if dtype is None else (dtype,))
     if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or (size is not None and t.shape[2] != size) or \
             (tokens is not None and t.shape[0] != tokens):
@@ -608,12 +640,18 @@ class Q4Matrix:
             _arg(levels, "levels", torch.bfloat16, numel=16)
         self.rows, self.D, self.group = rows, D, group
         self.codes, self.scales, self.offsets, self.levels = codes, scales, offsets, levels
+        self.device = codes.device
+        for name, t in (("scales", scales), ("offsets", offsets), ("levels", levels)):
+            if t is not None and t.device != codes.device:
+                raise ValueError(f"{name}: on {t.device}, the codes are on {codes.device}")
+        self._ws = {}   # workspace bytes by (batch, activation type, prologue)
         self.desc = rq_q4_matrix(rows, D, group, _TYPES[scales.dtype], *(t.data_ptr() if t is not None else None
                                                                          for t in (codes, scales, offsets, levels)))
+        self._ref = ctypes.byref(self.desc)
 
     @property
     def ref(self):
-        return ctypes.byref(self.desc)
+        return self._ref
 
     def resident_bytes(self):
         return sum(t.numel() * t.element_size() for t in (self.codes, self.scales, self.offsets, self.levels) if t is not None)
@@ -659,18 +697,24 @@ def q4_matvec(W, x, x2=None, prologue=RQ_PRO_NONE, ws=None, out=None):
     """rq_q4_matvec: y [B][rows] fp32 = W a for a Q4Matrix, a = x (float32, bfloat16 or float16) or gelu_tanh(x) * x2."""
     if not isinstance(W, Q4Matrix):
         raise TypeError("q4_matvec takes a Q4Matrix")
-    _typed(x, "x")
+    xt = _TYPES[_typed(x, "x").dtype]
     B = x.shape[0] if x.dim() == 2 else -1
-    _arg(x, "x", x.dtype, shape=(B, W.D))
+    _tensor(x, "x", x.dtype, (B, W.D))
     if x2 is not None:
-        _arg(x2, "x2", torch.float32, shape=(B, W.D))
-    y = out if out is not None else torch.empty((B, W.rows), dtype=torch.float32, device=x.device)
-    _arg(y, "out", torch.float32, numel=B * W.rows)
-    ws = _scratch(ws, q4_matvec_workspace(W, B, x.dtype, prologue), x.device)
-    dev = _one_device(x=x, x2=x2, out=y, ws=ws, codes=W.codes, scales=W.scales, offsets=W.offsets, levels=W.levels)
-    _call(lib().rq_q4_matvec, dev, W.ref, _ptr(x), _TYPES[x.dtype], _ptr(x2), prologue, B, _ptr(y), _ptr(ws),
+        _tensor(x2, "x2", torch.float32, (B, W.D))
+    if out is None:
+        out = torch.empty((B, W.rows), dtype=torch.float32, device=x.device)
+    else:
+        _arg(out, "out", torch.float32, numel=B * W.rows)
+    need = W._ws.get((B, xt, prologue))
+    if need is None:
+        need = W._ws[B, xt, prologue] = q4_matvec_workspace(W, B, x.dtype, prologue)
+    if need or ws is not None:
+        ws = _scratch(ws, need, x.device)
+    dev = _same_device("codes x x2 out ws", W.codes, x, x2, out, ws)
+    _call(lib().rq_q4_matvec, dev, W.ref, x.data_ptr(), xt, _at(x2), prologue, B, out.data_ptr(), _at(ws),
           ws.numel() if ws is not None else 0)
-    return y
+    return out
 
 
 class KVCache:
@@ -685,8 +729,12 @@ class KVCache:
         _arg(k, "k", k.dtype)
         _arg(v, "v", k.dtype, shape=(pages, kv_heads, head_dim, page_size))
         self.pages, self.kv_heads, self.page_size, self.head_dim = pages, kv_heads, page_size, head_dim
-        self.k, self.v, self.dtype = k, v, k.dtype
+        self.k, self.v, self.dtype, self.device = k, v, k.dtype, k.device
+        if v.device != k.device:
+            raise ValueError(f"v: on {v.device}, k is on {k.device}")
         self.desc = rq_kv_cache(pages, page_size, kv_heads, head_dim, _TYPES[k.dtype], k.data_ptr(), v.data_ptr())
+        self._ref = ctypes.byref(self.desc)
+        self._ws = {}   # attention's workspace bytes by its sizes
 
     @classmethod
     def empty(cls, pages, kv_heads, page_size, head_dim, dtype=torch.bfloat16, device="cuda"):
@@ -696,16 +744,16 @@ class KVCache:
 
     @property
     def ref(self):
-        return ctypes.byref(self.desc)
+        return self._ref
 
 
 def _batch(tokens, cu_q, lens, table):
     """The rq_seq_batch of int32 tensors cu_q [seqs + 1], lens [seqs], table [seqs][max_pages]."""
     seqs = lens.shape[0] if isinstance(lens, torch.Tensor) and lens.dim() == 1 else -1
-    _arg(lens, "lens", torch.int32, shape=(seqs,))
-    _arg(cu_q, "cu_q", torch.int32, shape=(seqs + 1,))
+    _tensor(lens, "lens", torch.int32, (seqs,))
+    _tensor(cu_q, "cu_q", torch.int32, (seqs + 1,))
     max_pages = table.shape[1] if isinstance(table, torch.Tensor) and table.dim() == 2 else -1
-    _arg(table, "table", torch.int32, shape=(seqs, max_pages))
+    _tensor(table, "table", torch.int32, (seqs, max_pages))
     return rq_seq_batch(seqs, tokens, max_pages, cu_q.data_ptr(), lens.data_ptr(), table.data_ptr())
 
 
@@ -718,16 +766,19 @@ def rope(x, positions, freqs, layout="half", mscale=1.0, inverse=False, out=None
     strided. out (contiguous heads, x's own memory allowed) or a new tensor of out_dtype (x's by default)."""
     xs = _heads_arg(x, "x")
     T, heads, size = x.shape
-    _arg(positions, "positions", torch.int32, shape=(T,))
-    _arg(freqs, "freqs", torch.float64, shape=(freqs.numel(),))
+    _tensor(positions, "positions", torch.int32, (T,))
+    half = freqs.numel()
+    _tensor(freqs, "freqs", torch.float64, (half,))
     if out is None:
         out = torch.empty((T, heads, size), dtype=out_dtype or x.dtype, device=x.device)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise ValueError(f"out: dtype {out.dtype}, expected {out_dtype}")
-    os_ = _heads_arg(out, "out", heads, size, T)
-    dev = _one_device(x=x, positions=positions, freqs=freqs, out=out)
-    _call(lib().rq_rope, dev, _ptr(x), _TYPES[x.dtype], T, heads, size, xs, _ptr(positions), _ptr(freqs), 2 * freqs.numel(),
-          _ROPE_LAYOUTS[layout], mscale, int(inverse), _ptr(out), _TYPES[out.dtype], os_)
+        os_ = heads * size
+    else:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError(f"out: dtype {out.dtype}, expected {out_dtype}")
+        os_ = _heads_arg(out, "out", heads, size, T)
+    dev = _same_device("x positions freqs out", x, positions, freqs, out)
+    _call(lib().rq_rope, dev, x.data_ptr(), _TYPES[x.dtype], T, heads, size, xs, positions.data_ptr(), freqs.data_ptr(), 2 * half,
+          _ROPE_LAYOUTS[layout], mscale, int(inverse), out.data_ptr(), _TYPES[out.dtype], os_)
     return out
 
 
@@ -735,22 +786,24 @@ def rope_append(q, k, v, cache, cu_q, lens, table, freqs, layout="half", mscale=
     """rq_rope_append: q rotated (returned, in the cache's type), k rotated and v stored in the KVCache at the places of the
     sequences' newest tokens. q [tokens][heads][size], k and v [tokens][kv_heads][size], of one type, tokens may be strided."""
     qs = _heads_arg(q, "q", size=cache.head_dim)
-    T, heads = q.shape[:2]
-    ks = _heads_arg(k, "k", cache.kv_heads, cache.head_dim, T, q.dtype)
-    vs = _heads_arg(v, "v", cache.kv_heads, cache.head_dim, T, q.dtype)
+    T, heads, size = q.shape
+    ks = _heads_arg(k, "k", cache.kv_heads, size, T, q.dtype)
+    vs = _heads_arg(v, "v", cache.kv_heads, size, T, q.dtype)
     batch = _batch(T, cu_q, lens, table)
-    _arg(freqs, "freqs", torch.float64, shape=(freqs.numel(),))
+    half = freqs.numel()
+    _tensor(freqs, "freqs", torch.float64, (half,))
     if positions is not None:
-        _arg(positions, "positions", torch.int32, shape=(T,))
+        _tensor(positions, "positions", torch.int32, (T,))
     if bad_pages is not None:
         _arg(bad_pages, "bad_pages", torch.int32, min_numel=1)
     if out is None:
-        out = torch.empty((T, heads, cache.head_dim), dtype=cache.dtype, device=q.device)
-    _arg(out, "out", cache.dtype, shape=(T, heads, cache.head_dim))
-    dev = _one_device(q=q, k=k, v=v, out=out, cache=cache.k, cache_v=cache.v, cu_q=cu_q, lens=lens, table=table, freqs=freqs,
-                      positions=positions, bad_pages=bad_pages)
-    _call(lib().rq_rope_append, dev, ctypes.byref(batch), cache.ref, _ptr(q), _ptr(k), _ptr(v), _TYPES[q.dtype], qs, ks, vs, heads,
-          _ptr(positions), _ptr(freqs), 2 * freqs.numel(), _ROPE_LAYOUTS[layout], mscale, _ptr(out), _ptr(bad_pages))
+        out = torch.empty((T, heads, size), dtype=cache.dtype, device=q.device)
+    else:
+        _tensor(out, "out", cache.dtype, (T, heads, size))
+    dev = _same_device("cache q k v out cu_q lens table freqs positions bad_pages", cache.k, q, k, v, out, cu_q, lens, table, freqs,
+                       positions, bad_pages)
+    _call(lib().rq_rope_append, dev, ctypes.byref(batch), cache.ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), _TYPES[q.dtype], qs, ks,
+          vs, heads, _at(positions), freqs.data_ptr(), 2 * half, _ROPE_LAYOUTS[layout], mscale, out.data_ptr(), _at(bad_pages))
     return out
 
 
@@ -764,19 +817,22 @@ def paged_attn(q, cache, cu_q, lens, table, scale=None, softcap=0.0, window=0, m
     q [tokens][heads][size] (tokens may be strided); scale defaults to size ** -0.5; max_len: an upper bound of lens if one
     is known; lse: a float32 [tokens][heads] tensor to fill."""
     qs = _heads_arg(q, "q", size=cache.head_dim, dtype=cache.dtype)
-    T, heads = q.shape[:2]
+    T, heads, size = q.shape
     batch = _batch(T, cu_q, lens, table)
     if out is None:
-        out = torch.empty((T, heads, cache.head_dim), dtype=cache.dtype, device=q.device)
-    _arg(out, "out", cache.dtype, shape=(T, heads, cache.head_dim))
+        out = torch.empty((T, heads, size), dtype=cache.dtype, device=q.device)
+    else:
+        _tensor(out, "out", cache.dtype, (T, heads, size))
     if lse is not None:
-        _arg(lse, "lse", torch.float32, shape=(T, heads))
+        _tensor(lse, "lse", torch.float32, (T, heads))
     if bad_pages is not None:
         _arg(bad_pages, "bad_pages", torch.int32, min_numel=1)
-    ws = _scratch(ws, paged_attn_workspace(cache, T, batch.seqs, heads, max_len), q.device)
-    dev = _one_device(q=q, out=out, cache=cache.k, cache_v=cache.v, cu_q=cu_q, lens=lens, table=table, lse=lse,
-                      bad_pages=bad_pages, ws=ws)
-    _call(lib().rq_paged_attn, dev, ctypes.byref(batch), cache.ref, _ptr(q), qs, heads,
-          cache.head_dim ** -0.5 if scale is None else scale, softcap, window, max_len, _ptr(out), _ptr(lse), _ptr(bad_pages),
-          _ptr(ws), ws.numel() if ws is not None else 0)
+    need = cache._ws.get((T, batch.seqs, heads, max_len))
+    if need is None:
+        need = cache._ws[T, batch.seqs, heads, max_len] = paged_attn_workspace(cache, T, batch.seqs, heads, max_len)
+    if need or ws is not None:
+        ws = _scratch(ws, need, q.device)
+    dev = _same_device("cache q out cu_q lens table lse bad_pages ws", cache.k, q, out, cu_q, lens, table, lse, bad_pages, ws)
+    _call(lib().rq_paged_attn, dev, ctypes.byref(batch), cache.ref, q.data_ptr(), qs, heads, size ** -0.5 if scale is None else scale,
+          softcap, window, max_len, out.data_ptr(), _at(lse), _at(bad_pages), _at(ws), ws.numel() if ws is not None else 0)
     return out
