@@ -8,12 +8,14 @@
 // Angles: position * freqs[i] in 64 bits, as turns, reduced to half a turn before the fp32 sine and cosine:
 // at position 10^6 a 32-bit product would already be off by a tenth of a radian.
 //
-// Bound: HBM; every value is read and written once. A workgroup takes up to 16
-// tokens, computes their cosines and sines once into LDS for all heads, then walks over (token, head, 8 values)
-// with 16-byte accesses. The cache keeps V transposed inside a page ([head size][page size], the layout that attention's matrix product
-// reads without a transpose): a tile of 16 positions is aligned to 16, so it lies in one page, and a thread
-// gathers one column's 16 values (reads are coalesced over the columns) into 16-byte stores.
-// The grid's second axis splits a tile's items where there are few tiles.
+// Bound: HBM; every value is read and written once. Tiles are 64 consecutive places of a sequence (or tokens, without a cache). A
+// workgroup takes up to 16 of a tile's tokens and a share of the heads, puts the cosines and sines into LDS once, and each thread
+// keeps those of one token and 8 values (16-byte accesses) while it walks over the heads, four heads' loads under way at a time.
+//
+// The cache keeps V transposed inside a page ([head size][page size], the layout that attention's matrix product reads without a transpose):
+// other workgroups of the same tile take 64 columns at a time through LDS, so that reads run along the columns and writes along the places,
+// 128 bytes each. Few tokens are written value by value.
+// The grid's second axis is these shares: more of them where there are few tiles.
 #include "rq_internal.h"
 
 namespace rq {
@@ -22,7 +24,8 @@ namespace {
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeTile = 16;   // positions of a tile; page sizes are multiples of it
+constexpr int kRopeTile = 64;   // places of a tile
+constexpr int kTurns = 2048;    // angles of a workgroup
 
 struct RopeArgs {
   const void *q, *k, *v;          // [tokens][heads][size], token strides below; k, v only with a cache
@@ -36,198 +39,298 @@ struct RopeArgs {
   void* out;
   rq_seq_batch batch;
   rq_kv_cache cache;
+  int page_shift;
   int32_t* bad;
+  int run;                        // tokens of a workgroup for q and k
+  int runs, shares, v_shares;     // workgroups of a tile: runs of tokens, shares of the heads for each, shares of v's columns
 };
 
-__device__ __forceinline__ float load1(const void* p, int dtype, int64_t i) {
-  if (dtype == RQ_F32) return static_cast<const float*>(p)[i];
-  if (dtype == RQ_BF16) return bf16_to_f32(static_cast<const uint16_t*>(p)[i]);
-  return (float)static_cast<const _Float16*>(p)[i];
+__device__ __forceinline__ float half_to_f32(uint32_t h, int dtype) {
+  return dtype == RQ_BF16 ? bf16_to_f32(h) : (float)__builtin_bit_cast(_Float16, (uint16_t)h);
 }
-__device__ __forceinline__ uint16_t pack1(float v, int dtype) {
+__device__ __forceinline__ uint32_t f32_to_half(float v, int dtype) {
   return dtype == RQ_BF16 ? f32_to_bf16(v) : __builtin_bit_cast(uint16_t, (_Float16)v);
 }
-__device__ __forceinline__ void store1(void* p, int dtype, int64_t i, float v) {
-  if (dtype == RQ_F32) static_cast<float*>(p)[i] = v;
-  else static_cast<uint16_t*>(p)[i] = pack1(v, dtype);
-}
-template <int VEC>
-__device__ __forceinline__ void load_vec(const void* p, int dtype, int64_t i, float (&v)[VEC]) {
-  if constexpr (VEC == 1) {
-    v[0] = load1(p, dtype, i);
-  } else if (dtype == RQ_F32) {
-    const u32x4* s = reinterpret_cast<const u32x4*>(static_cast<const float*>(p) + i);
-    const u32x4 a = s[0], b = s[1];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[j] = __uint_as_float(a[j]);
-      v[4 + j] = __uint_as_float(b[j]);
-    }
-  } else {
-    const u32x4 a = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + i);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t lo = a[j] & 0xffffu, hi = a[j] >> 16;
-      v[2 * j] = dtype == RQ_BF16 ? bf16_to_f32(lo) : (float)__builtin_bit_cast(_Float16, (uint16_t)lo);
-      v[2 * j + 1] = dtype == RQ_BF16 ? bf16_to_f32(hi) : (float)__builtin_bit_cast(_Float16, (uint16_t)hi);
-    }
-  }
-}
-template <int VEC>
-__device__ __forceinline__ void store_vec(void* p, int dtype, int64_t i, const float (&v)[VEC]) {
-  if constexpr (VEC == 1) {
-    store1(p, dtype, i, v[0]);
-  } else if (dtype == RQ_F32) {
-    u32x4* d = reinterpret_cast<u32x4*>(static_cast<float*>(p) + i);
-    d[0] = u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
-    d[1] = u32x4{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])};
-  } else {
-    u32x4 a;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) a[j] = pack1(v[2 * j], dtype) | ((uint32_t)pack1(v[2 * j + 1], dtype) << 16);
-    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + i) = a;
-  }
-}
 
-// VEC values a thread and access: 8 (16-byte accesses of 16-bit types) or 1.
-template <int VEC, bool INTERLEAVED>
-__global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a, int append) {
-  extern __shared__ __align__(16) float2 turn[];   // [tokens of the tile][half]
-  __shared__ int tile_pos[kRopeTile];              // place in the sequence
-  const int tid = threadIdx.x;
-  // this tile's tokens: [t0, t0 + n), all of one sequence, in one page, with a cache
-  int t0, n, place0 = 0, page = -1;
-  if (append) {   // (uniform)
-    const SeqTile st = find_tile(a.batch, kRopeTile, 2, (int)blockIdx.x);
-    if (st.seq < 0) return;
-    const int new0 = st.len - st.n;                                       // place of the sequence's first new token (may be < 0)
-    const int lo = (floor_div(new0, kRopeTile) + st.tile) * kRopeTile;    // the tile's places: lo .. lo + 15
-    const int first = max(lo, new0), end = min(lo + kRopeTile, st.len);
-    if (first >= end) return;
-    t0 = st.t0 + (first - new0);
-    n = end - first;
-    place0 = first;
-    const int pi = lo >= 0 ? lo / a.cache.page_size : -1;
-    if (pi >= 0 && pi < a.batch.max_pages) page = a.batch.table[(int64_t)st.seq * a.batch.max_pages + pi];
-    if ((unsigned)page >= (unsigned)a.cache.pages) {
-      page = -1;
-      if (a.bad && tid == 0 && blockIdx.y == 0) atomicAdd(a.bad, n);
+// VEC values (8 or 1) as they lie in memory.
+template <int VEC, bool WIDE>
+struct Raw {
+  static constexpr int N = VEC == 1 ? 1 : WIDE ? 8 : 4;
+  uint32_t w[N];
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    if constexpr (VEC == 1) {
+      if constexpr (WIDE) w[0] = static_cast<const uint32_t*>(p)[i];
+      else w[0] = static_cast<const uint16_t*>(p)[i];
+    } else {
+      const u32x4* s = reinterpret_cast<const u32x4*>(static_cast<const unsigned char*>(p) + i * (WIDE ? 4 : 2));
+#pragma unroll
+      for (int j = 0; j < N; j += 4) {
+        const u32x4 v = s[j / 4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[j + e] = v[e];
+      }
     }
-  } else {
-    t0 = (int)blockIdx.x * kRopeTile;
-    n = min(kRopeTile, a.tokens - t0);
   }
-  if (tid < n) tile_pos[tid] = a.positions ? a.positions[t0 + tid] : place0 + tid;
-  __syncthreads();
+  __device__ __forceinline__ float get(int j, int dtype) const {
+    if constexpr (WIDE) return __uint_as_float(w[j]);
+    if constexpr (VEC == 1) return half_to_f32(w[0], dtype);
+    return half_to_f32((w[j / 2] >> (16 * (j & 1))) & 0xffffu, dtype);
+  }
+  __device__ __forceinline__ void set(int j, float v, int dtype) {   // in the order of j
+    if constexpr (WIDE) w[j] = __float_as_uint(v);
+    else if constexpr (VEC == 1) w[0] = f32_to_half(v, dtype);
+    else if (j & 1) w[j / 2] |= f32_to_half(v, dtype) << 16;
+    else w[j / 2] = f32_to_half(v, dtype);
+  }
+  __device__ __forceinline__ void store(void* p, int64_t i) const {
+    if constexpr (VEC == 1) {
+      if constexpr (WIDE) static_cast<uint32_t*>(p)[i] = w[0];
+      else static_cast<uint16_t*>(p)[i] = (uint16_t)w[0];
+    } else {
+      u32x4* d = reinterpret_cast<u32x4*>(static_cast<unsigned char*>(p) + i * (WIDE ? 4 : 2));
+#pragma unroll
+      for (int j = 0; j < N; j += 4) d[j / 4] = u32x4{w[j], w[j + 1], w[j + 2], w[j + 3]};
+    }
+  }
+};
+
+// The tile's tokens [t0, t0 + n), all of one sequence, at its places place0 .. (with a cache).
+struct RopeTile {
+  int t0, n, place0;
+  const int32_t* table;
+  // the page of a place, or -1
+  __device__ __forceinline__ int page(const RopeArgs& a, int place) const {
+    if (place < 0 || (place >> a.page_shift) >= a.batch.max_pages) return -1;
+    const int p = table[place >> a.page_shift];
+    return (unsigned)p < (unsigned)a.cache.pages ? p : -1;
+  }
+};
+
+// q and k: heads [h0, h1) of tokens [ta, tb) of the tile (k's heads behind q's).
+template <int VEC, bool INTERLEAVED, bool IN32, bool OUT32>
+__device__ __forceinline__ void rotate_heads(const RopeArgs& a, const RopeTile& tile, bool append, int ta, int tb, int h0, int h1,
+                                             float2* turn) {
+  constexpr int F = VEC == 1 ? 1 : INTERLEAVED ? VEC / 2 : VEC;   // angles of an item
+  constexpr int AHEAD = VEC == 1 ? 2 : 4;                          // heads whose loads are under way
+  constexpr bool TWO = VEC == 1 || !INTERLEAVED;                   // the pairs' second values are a run of their own
+  const int rot = 2 * a.half;
+  const int turned = INTERLEAVED ? (VEC == 1 ? a.half : rot / VEC) : a.half / VEC;   // rotated items of a head
+  const int per_head = turned + (a.size - rot) / VEC;                                // and those that pass
+  const int tid = threadIdx.x, n = tb - ta;
   for (int i = tid; i < n * a.half; i += kRopeThreads) {
     const int t = i / a.half;
-    double turns = (double)tile_pos[t] * (a.freqs[i - t * a.half] * 0.15915494309189533577);   // 1 / (2 pi)
+    const double position = a.positions ? a.positions[tile.t0 + ta + t] : tile.place0 + ta + t;
+    double turns = position * (a.freqs[i - t * a.half] * 0.15915494309189533577);   // 1 / (2 pi)
     turns -= rint(turns);
     float s, c;
     sincospif((float)(2.0 * turns), &s, &c);
     turn[i] = make_float2(c * a.mscale, (a.inverse ? -s : s) * a.mscale);
   }
   __syncthreads();
-
-  const int rot = 2 * a.half;
-  const int turned = INTERLEAVED ? rot / (VEC == 1 ? 2 : VEC) : a.half / VEC;   // rotated items of a head
-  const int per_head = turned + (a.size - rot) / VEC;                           // and those that pass
-  const int hk = append ? a.kv_heads : 0;
-  const int items = n * (a.heads + hk) * per_head;
-  const int vitems = hk * a.size;                                               // columns of V
-  const int share = (items + vitems + (int)gridDim.y - 1) / (int)gridDim.y;
-  const int it0 = (int)blockIdx.y * share, it1 = min(items + vitems, it0 + share);
-  const int place_in_page = page >= 0 ? place0 % a.cache.page_size : 0;
-  for (int it = it0 + tid; it < it1; it += kRopeThreads) {
-    if (it < items) {
-      const int c = it % per_head, th = it / per_head;
-      const int h = th % (a.heads + hk), t = th / (a.heads + hk);
-      const bool is_k = h >= a.heads;
-      const void* src = is_k ? a.k : a.q;
-      const int64_t from = (int64_t)(t0 + t) * (is_k ? a.k_stride : a.q_stride) + (int64_t)(is_k ? h - a.heads : h) * a.size;
-      void* dst = is_k ? a.cache.k : a.out;
-      int64_t to = (int64_t)(t0 + t) * a.o_stride + (int64_t)h * a.size;
-      if (is_k) {
-        if (page < 0) continue;
-        to = (((int64_t)page * hk + (h - a.heads)) * a.cache.page_size + place_in_page + t) * a.size;
-      }
-      const float2* tr = turn + t * a.half;
-      if (c >= turned) {
-        const int i = rot + (c - turned) * VEC;
-        float x[VEC];
-        load_vec<VEC>(src, a.in_dtype, from + i, x);
-        store_vec<VEC>(dst, a.out_dtype, to + i, x);
-      } else if constexpr (!INTERLEAVED) {
-        const int i = c * VEC;
-        float x1[VEC], x2[VEC], y1[VEC], y2[VEC];
-        load_vec<VEC>(src, a.in_dtype, from + i, x1);
-        load_vec<VEC>(src, a.in_dtype, from + a.half + i, x2);
+  // threads: items of a head, then tokens, then heads side by side
+  const int wide = min(per_head, kRopeThreads);
+  const int slots = kRopeThreads / wide, slot = tid / wide;
+  const int ts = min(n, slots), hs = slots / ts;
+  if (slot >= ts * hs) return;
+  const int first_head = h0 + slot / ts;
+  for (int c = tid - slot * wide; c < per_head; c += wide) {
+    const bool turns = c < turned;
+    // where the item's values lie in a head: one run of VEC, or two that are rot/2 apart
+    const int at = !turns ? rot + (c - turned) * VEC : INTERLEAVED && VEC == 1 ? 2 * c : c * VEC;
+    const int second = turns ? (INTERLEAVED ? (VEC == 1 ? 1 : 0) : a.half) : 0;   // distance of the second run (0: none)
+    for (int t = ta + slot % ts; t < tb; t += ts) {
+      const int token = tile.t0 + t;
+      float cs[F], sn[F];
+      if (turns) {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const float2 cs = tr[i + j];
-          y1[j] = x1[j] * cs.x - x2[j] * cs.y;
-          y2[j] = x2[j] * cs.x + x1[j] * cs.y;
+        for (int j = 0; j < F; ++j) {
+          const float2 v = turn[(t - ta) * a.half + (VEC == 1 ? c : c * F) + j];
+          cs[j] = v.x;
+          sn[j] = v.y;
         }
-        store_vec<VEC>(dst, a.out_dtype, to + i, y1);
-        store_vec<VEC>(dst, a.out_dtype, to + a.half + i, y2);
-      } else if constexpr (VEC == 1) {
-        const float x1 = load1(src, a.in_dtype, from + 2 * c), x2 = load1(src, a.in_dtype, from + 2 * c + 1);
-        const float2 cs = tr[c];
-        store1(dst, a.out_dtype, to + 2 * c, x1 * cs.x - x2 * cs.y);
-        store1(dst, a.out_dtype, to + 2 * c + 1, x2 * cs.x + x1 * cs.y);
-      } else {
-        const int i = c * VEC;
-        float x[VEC], y[VEC];
-        load_vec<VEC>(src, a.in_dtype, from + i, x);
-#pragma unroll
-        for (int j = 0; j < VEC; j += 2) {
-          const float2 cs = tr[(i + j) / 2];
-          y[j] = x[j] * cs.x - x[j + 1] * cs.y;
-          y[j + 1] = x[j + 1] * cs.x + x[j] * cs.y;
-        }
-        store_vec<VEC>(dst, a.out_dtype, to + i, y);
       }
-    } else if (page >= 0) {
-      const int d = it - items;   // column of V: (head, place in the head)
-      const int h = d / a.size, e = d - h * a.size;
-      const int64_t from = (int64_t)t0 * a.v_stride + d;
-      uint16_t* dst = static_cast<uint16_t*>(a.cache.v) + (((int64_t)page * hk + h) * a.size + e) * a.cache.page_size + place_in_page;
-      if (n == kRopeTile) {
-        uint32_t w[kRopeTile / 2];
+      int page = -1;
+      if (append) page = tile.page(a, tile.place0 + t);
+      const int64_t in_page = append ? ((tile.place0 + t) & ((1 << a.page_shift) - 1)) : 0;
+      for (int h = first_head; h < h1; h += AHEAD * hs) {
+        Raw<VEC, IN32> x1[AHEAD], x2[AHEAD];
 #pragma unroll
-        for (int t = 0; t < kRopeTile; t += 2)
-          w[t / 2] = pack1(load1(a.v, a.in_dtype, from + t * a.v_stride), a.out_dtype) |
-                     ((uint32_t)pack1(load1(a.v, a.in_dtype, from + (t + 1) * a.v_stride), a.out_dtype) << 16);
-        reinterpret_cast<u32x4*>(dst)[0] = u32x4{w[0], w[1], w[2], w[3]};
-        reinterpret_cast<u32x4*>(dst)[1] = u32x4{w[4], w[5], w[6], w[7]};
-      } else {
-        for (int t = 0; t < n; ++t) dst[t] = pack1(load1(a.v, a.in_dtype, from + t * a.v_stride), a.out_dtype);
+        for (int u = 0; u < AHEAD; ++u) {
+          const int g = min(h + u * hs, h1 - 1);   // (behind the last: that one again, not stored)
+          const bool is_k = g >= a.heads;
+          const void* src = is_k ? a.k : a.q;
+          const int64_t from = (int64_t)token * (is_k ? a.k_stride : a.q_stride) + (int64_t)(is_k ? g - a.heads : g) * a.size + at;
+          x1[u].load(src, from);
+          if constexpr (TWO) x2[u].load(src, from + second);
+        }
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+          const int g = h + u * hs;
+          if (g >= h1) break;
+          const bool is_k = g >= a.heads;
+          if (is_k && page < 0) continue;
+          void* dst = is_k ? a.cache.k : a.out;
+          const int64_t to = at + (is_k ? ((((int64_t)page * a.kv_heads + (g - a.heads)) << a.page_shift) + in_page) * a.size
+                                        : (int64_t)token * a.o_stride + (int64_t)g * a.size);
+          Raw<VEC, OUT32> y1, y2;
+          if (!turns) {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) y1.set(j, x1[u].get(j, a.in_dtype), a.out_dtype);
+          } else if constexpr (INTERLEAVED && VEC > 1) {
+#pragma unroll
+            for (int j = 0; j < VEC; j += 2) {
+              const float p = x1[u].get(j, a.in_dtype), q = x1[u].get(j + 1, a.in_dtype);
+              y1.set(j, p * cs[j / 2] - q * sn[j / 2], a.out_dtype);
+              y1.set(j + 1, q * cs[j / 2] + p * sn[j / 2], a.out_dtype);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+              const float p = x1[u].get(j, a.in_dtype), q = x2[u].get(j, a.in_dtype);
+              y1.set(j, p * cs[j % F] - q * sn[j % F], a.out_dtype);
+              y2.set(j, q * cs[j % F] + p * sn[j % F], a.out_dtype);
+            }
+          }
+          y1.store(dst, to);
+          if (second) y2.store(dst, to + second);
+        }
       }
     }
   }
 }
 
+// v: columns [d0, d1) of the tile's tokens, through LDS 64 at a time where there are many tokens.
+template <bool VEC, bool IN32>
+__device__ __forceinline__ void transpose_columns(const RopeArgs& a, const RopeTile& tile, int d0, int d1, uint16_t (*lds)[kRopeTile + 8]) {
+  const int tid = threadIdx.x;
+  const int mask = (1 << a.page_shift) - 1;
+  uint16_t* cache = static_cast<uint16_t*>(a.cache.v);
+  auto value = [&](int t, int d) {
+    Raw<1, IN32> x;
+    x.load(a.v, (int64_t)(tile.t0 + t) * a.v_stride + d);
+    return (uint16_t)f32_to_half(x.get(0, a.in_dtype), a.out_dtype);
+  };
+  // where column d (of all kv heads) of a place's page begins, and the place in it
+  auto spot = [&](int page, int d, int place) {
+    const int h = d / a.size;
+    return ((((int64_t)page * a.kv_heads + h) * a.size + (d - h * a.size)) << a.page_shift) + (place & mask);
+  };
+  if (tile.n < 8 || !VEC) {
+    for (int d = d0 + tid; d < d1; d += kRopeThreads)
+      for (int t = 0; t < tile.n; ++t) {
+        const int page = tile.page(a, tile.place0 + t);
+        if (page >= 0) cache[spot(page, d, tile.place0 + t)] = value(t, d);
+      }
+    return;
+  }
+  const int lead = tile.place0 & (kRopeTile - 1);   // the tile's first place among its 64
+  for (int c0 = d0; c0 < d1; c0 += 64) {
+    const int cols = min(64, d1 - c0);               // a multiple of 8
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int t = tid / 8 + 32 * i, c = 8 * (tid % 8);   // token of the tile, its 8 columns
+      if (t < tile.n && c < cols) {
+        Raw<8, IN32> x;
+        x.load(a.v, (int64_t)(tile.t0 + t) * a.v_stride + c0 + c);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) lds[c + j][lead + t] = (uint16_t)f32_to_half(x.get(j, a.in_dtype), a.out_dtype);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int c = tid / 8 + 32 * i, p = 8 * (tid % 8);   // column, its 8 places
+      const int lo = max(p, lead), hi = min(p + 8, lead + tile.n);
+      if (c < cols && lo < hi) {
+        const int place = tile.place0 - lead + p;          // (8 places of a multiple of 8 lie in one page)
+        const int page = tile.page(a, place + (lo - p));
+        if (page >= 0) {
+          uint16_t* dst = cache + spot(page, c0 + c, place);
+          if (hi - lo == 8) *reinterpret_cast<u32x4*>(dst) = *reinterpret_cast<const u32x4*>(&lds[c][p]);
+          else
+            for (int j = lo; j < hi; ++j) dst[j - p] = lds[c][j];
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// VEC values a thread and access: 8 (16-byte accesses of 16-bit types) or 1.
+template <int VEC, bool INTERLEAVED, bool IN32, bool OUT32>
+__global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a, int append) {
+  __shared__ __align__(16) float2 lds[kTurns];   // angles, or v's columns
+  RopeTile tile;
+  if (append) {   // (uniform)
+    const SeqTile st = find_tile(a.batch, kRopeTile, 2, (int)blockIdx.x);
+    if (st.seq < 0) return;
+    const int new0 = st.len - st.n;                                       // place of the sequence's first new token (may be < 0)
+    const int lo = (floor_div(new0, kRopeTile) + st.tile) * kRopeTile;    // the tile's places: lo .. lo + 63
+    const int first = max(lo, new0), end = min(lo + kRopeTile, st.len);
+    if (first >= end) return;
+    tile.t0 = st.t0 + (first - new0);
+    tile.n = end - first;
+    tile.place0 = first;
+    tile.table = a.batch.table + (int64_t)st.seq * a.batch.max_pages;
+    if (a.bad && blockIdx.y == 0 && (int)threadIdx.x < tile.n && tile.page(a, first + (int)threadIdx.x) < 0) atomicAdd(a.bad, 1);
+  } else {
+    tile.t0 = (int)blockIdx.x * kRopeTile;
+    tile.n = min(kRopeTile, a.tokens - tile.t0);
+    tile.place0 = 0;
+    tile.table = nullptr;
+  }
+  const int share = blockIdx.y;
+  if (share < a.runs * a.shares) {
+    const int all = a.heads + (append ? a.kv_heads : 0), each = (all + a.shares - 1) / a.shares;
+    const int run = share / a.shares, h0 = (share - run * a.shares) * each, h1 = min(all, h0 + each);
+    const int ta = run * a.run, tb = min(tile.n, ta + a.run);
+    if (h0 < h1 && ta < tb) rotate_heads<VEC, INTERLEAVED, IN32, OUT32>(a, tile, append, ta, tb, h0, h1, lds);
+  } else {
+    const int all = a.kv_heads * a.size, each = ((all + a.v_shares - 1) / a.v_shares + 63) / 64 * 64;
+    const int d0 = (share - a.runs * a.shares) * each, d1 = min(all, d0 + each);
+    if (d0 < d1) transpose_columns<VEC == 8, IN32>(a, tile, d0, d1, reinterpret_cast<uint16_t(*)[kRopeTile + 8]>(lds));
+  }
+}
+
 bool aligned16(const void* p) { return (uintptr_t)p % 16 == 0; }
 
-hipError_t launch(const RopeArgs& a, bool interleaved, int append, int tiles, hipStream_t stream) {
+template <int VEC, bool INTERLEAVED>
+void launch_types(const RopeArgs& a, int append, dim3 grid, hipStream_t stream) {
+  const dim3 block(kRopeThreads);
+  if (a.in_dtype == RQ_F32) {
+    if (a.out_dtype == RQ_F32) hipLaunchKernelGGL((rope_kernel<VEC, INTERLEAVED, true, true>), grid, block, 0, stream, a, append);
+    else hipLaunchKernelGGL((rope_kernel<VEC, INTERLEAVED, true, false>), grid, block, 0, stream, a, append);
+  } else {
+    if (a.out_dtype == RQ_F32) hipLaunchKernelGGL((rope_kernel<VEC, INTERLEAVED, false, true>), grid, block, 0, stream, a, append);
+    else hipLaunchKernelGGL((rope_kernel<VEC, INTERLEAVED, false, false>), grid, block, 0, stream, a, append);
+  }
+}
+
+hipError_t launch(RopeArgs& a, bool interleaved, int append, int tiles, hipStream_t stream) {
   const int ib = a.in_dtype == RQ_F32 ? 4 : 2, ob = a.out_dtype == RQ_F32 ? 4 : 2;
   // 16-byte accesses where every row and every half begins at 16 bytes and holds whole 8s
   bool vec = a.size % 8 == 0 && (interleaved ? 2 * a.half : a.half) % 8 == 0 && aligned16(a.q) && aligned16(a.out) &&
              a.q_stride * ib % 16 == 0 && a.o_stride * ob % 16 == 0;
-  if (append) vec = vec && aligned16(a.k) && a.k_stride * ib % 16 == 0;
-  // enough workgroups for the chip where there are few tiles: at least 256 items each
-  const int64_t items = (int64_t)(a.heads + (append ? 2 * a.kv_heads : 0)) * a.size / (vec ? 8 : 1) *
-                        std::min(kRopeTile, std::max(1, a.tokens / std::max(1, append ? a.batch.seqs : 1)));
-  const int64_t want = (4 * kCUs + tiles - 1) / tiles;
-  const int parts = (int)std::max<int64_t>(1, std::min(want, items / kRopeThreads));
-  const size_t lds = (size_t)kRopeTile * a.half * sizeof(float2);
-  const dim3 grid((unsigned)tiles, (unsigned)parts), block(kRopeThreads);
+  if (append) vec = vec && aligned16(a.k) && a.k_stride * ib % 16 == 0 && aligned16(a.v) && a.v_stride * ib % 16 == 0;
+  // Workgroups of a tile. A thread that keeps its angles walks over at least four heads where there are tokens enough; about 8
+  // workgroups a CU beyond that do not pay, since each computes its angles again. (append of 8,100 tokens x 40 heads x 128: 43 us with two
+  // heads a share and v in one share, the figure below with these.)
+  const int all = a.heads + (append ? a.kv_heads : 0);
+  const int per_tile = std::min(kRopeTile, append ? std::max(1, a.tokens / std::max(1, a.batch.seqs)) : a.tokens);   // tokens
+  a.run = std::min(16, kTurns / a.half);
+  a.runs = (std::min(kRopeTile, append ? kRopeTile : a.tokens) + a.run - 1) / a.run;
+  const int per_head = (interleaved ? (vec ? 2 * a.half / 8 : a.half) : a.half / (vec ? 8 : 1)) + (a.size - 2 * a.half) / (vec ? 8 : 1);
+  const int side = std::max(1, kRopeThreads / std::max(1, std::min(per_head, kRopeThreads)) / std::min(per_tile, a.run));   // heads side by side
+  const int busy = append ? std::min(tiles, a.tokens / kRopeTile + a.batch.seqs) : tiles;
+  a.shares = std::max(1, std::min(all / (4 * side), 8 * kCUs / std::max(1, busy * ((per_tile + a.run - 1) / a.run))));
+  a.v_shares = append ? std::max(1, std::min((a.kv_heads * a.size + 63) / 64, 8 * kCUs / std::max(1, busy))) : 0;
+  const dim3 grid((unsigned)tiles, (unsigned)(a.runs * a.shares + a.v_shares));
   if (interleaved) {
-    if (vec) hipLaunchKernelGGL((rope_kernel<8, true>), grid, block, lds, stream, a, append);
-    else hipLaunchKernelGGL((rope_kernel<1, true>), grid, block, lds, stream, a, append);
+    if (vec) launch_types<8, true>(a, append, grid, stream);
+    else launch_types<1, true>(a, append, grid, stream);
   } else {
-    if (vec) hipLaunchKernelGGL((rope_kernel<8, false>), grid, block, lds, stream, a, append);
-    else hipLaunchKernelGGL((rope_kernel<1, false>), grid, block, lds, stream, a, append);
+    if (vec) launch_types<8, false>(a, append, grid, stream);
+    else launch_types<1, false>(a, append, grid, stream);
   }
   return hipGetLastError();
 }
@@ -281,6 +384,7 @@ hipError_t launch_rope_append(const rq_seq_batch* batch, const rq_kv_cache* cach
   a.batch = *batch;
   a.cache = *cache;
   a.bad = bad;
+  a.page_shift = __builtin_ctz((unsigned)cache->page_size);
   return launch(a, layout == RQ_ROPE_INTERLEAVED, 1, batch->tokens / kRopeTile + 2 * batch->seqs, stream);
 }
 
