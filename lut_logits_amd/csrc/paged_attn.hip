@@ -108,6 +108,7 @@ __device__ __forceinline__ int page_of(const AttnArgs& a, const int32_t* table, 
 // 64 entries of a sequence's table, one a lane (-1: no page): one load for many tiles instead of a wait in each.
 struct PageWindow {
   int first = 0, id = -1;
+  uint64_t missing = 0;   // (uniform) a bit for each entry without a page
   __device__ __forceinline__ void load(const AttnArgs& a, const int32_t* table, int entry) {
     first = entry;
     const int i = entry + (int)(threadIdx.x & 63);
@@ -116,6 +117,11 @@ struct PageWindow {
       const int p = table[i];
       if ((unsigned)p < (unsigned)a.cache.pages) id = p;
     }
+    missing = __ballot(id < 0);
+  }
+  // whether entries [a, b] all have pages (uniform)
+  __device__ __forceinline__ bool all(int a, int b) const {
+    return ((missing >> (a - first)) & ((2ull << (b - a)) - 1)) == 0;
   }
   __device__ __forceinline__ bool holds(int entry) const { return (unsigned)(entry - first) < 64u; }
   __device__ __forceinline__ int at(int entry) const { return __builtin_amdgcn_readlane(id, entry - first); }      // entry uniform
@@ -495,24 +501,38 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 4))
     const int k_lane = key_of_row(kx & 15) * DH + 8 * ((tid % KC) ^ (kx & 7));
     const int vx = tid / VC;
     const int v_keys = 8 * ((tid % VC) ^ (VC == 8 ? (vx & 7) : ((vx >> 1) & 3)));
-    auto copy = [&](int b, int t) {
-      unsigned char* kd = smem + (size_t)b * 2 * CH * 16 + wave * 1024;
-      unsigned char* vd = kd + (size_t)CH * 16;
+    constexpr int kRows = kThreads / KC;                        // K rows of 256 chunks: 8, 16 or 32
+    // rows of chunk block j: their first key, less what the lane adds
+    auto k_key = [&](int j) {
+      return kRows == 8 ? 16 * (j >> 1) + 4 * (j & 1) : kRows * j + (kRows == 32 ? (wave * 8 & ~15) : 0);
+    };
+    const bool one_page = BK <= 1 << a.page_shift;              // a tile lies in one page (uniform)
+    const int v_lane = (vx << a.page_shift) + v_keys;
+    auto put = [&](const uint16_t* src, unsigned char* dst) {
+      __builtin_amdgcn_global_load_lds((const void*)src, (lds_ptr_t)dst, 16, 0, 0);
+    };
+    constexpr int NC = CH / kThreads;                           // copies of a thread for K, and for V
+    auto copy_k = [&](int b, int t) {
+      unsigned char* dst = smem + (size_t)b * 2 * CH * 16 + wave * 1024;
+      if (one_page) {
+        const uint16_t* ks = kbase + (int64_t)max(0, win.at(entry(BK * t))) * page_elems + (int64_t)((BK * t) & pmask) * DH;
 #pragma unroll
-      for (int j = 0; j < CH / kThreads; ++j) {
-        constexpr int kRows = kThreads / KC;                    // rows of 256 chunks: 8, 16 or 32
-        const int i0 = kRows * j + (kRows == 32 ? (wave * 8 & ~15) : 0);
-        const int g = i0 >> 4;                                  // 16 keys (uniform)
-        const int pg = win.at(entry(BK * t + 16 * g));
-        const uint16_t* src = kbase + (int64_t)max(0, pg) * page_elems + (int64_t)(((BK * t + 16 * g) & pmask) + (kRows == 8 ? 4 * (j & 1) : 0)) * DH;
-        __builtin_amdgcn_global_load_lds((const void*)(src + k_lane), (lds_ptr_t)(kd + (size_t)j * kThreads * 16), 16, 0, 0);
+        for (int j = 0; j < NC; ++j) put(ks + k_key(j) * DH + k_lane, dst + j * kThreads * 16);
+      } else {
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+          const int key = BK * t + (k_key(j) & ~15);
+          put(kbase + (int64_t)max(0, win.at(entry(key))) * page_elems + (int64_t)((key & pmask) + (k_key(j) & 15)) * DH + k_lane, dst + j * kThreads * 16);
+        }
       }
-      const int pg = win.at_lane(entry(BK * t + v_keys));
-      const uint16_t* src = vbase + (int64_t)max(0, pg) * page_elems + ((int64_t)vx << a.page_shift) + ((BK * t + v_keys) & pmask);
+    };
+    auto copy_v = [&](int b, int t) {
+      unsigned char* dst = smem + (size_t)b * 2 * CH * 16 + CH * 16 + wave * 1024;
+      const uint16_t* vs = one_page ? vbase + (int64_t)max(0, win.at(entry(BK * t))) * page_elems + ((BK * t) & pmask) + v_lane
+                                    : vbase + (int64_t)max(0, win.at_lane(entry(BK * t + v_keys))) * page_elems +
+                                          ((BK * t + v_keys) & pmask) + (vx << a.page_shift);
 #pragma unroll
-      for (int j = 0; j < CH / kThreads; ++j)
-        __builtin_amdgcn_global_load_lds((const void*)(src + ((int64_t)(kThreads / VC * j) << a.page_shift)),
-                                         (lds_ptr_t)(vd + (size_t)j * kThreads * 16), 16, 0, 0);
+      for (int j = 0; j < NC; ++j) put(vs + ((kThreads / VC * j) << a.page_shift), dst + j * kThreads * 16);
     };
     // where this lane reads: chunk 2k + h of row i32 of K, chunk 4u + 2g + h of row i32 of V, both swizzled; the even parts of the
     // chunk numbers are flipped in by the reader
@@ -522,17 +542,41 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 4))
     // One tile from buffer b. whole: every row of the wave sees every key
     auto attend = [&](int b, int t, bool whole) {
       const uint32_t kl = k_read + b * (2 * CH * 16), vl = v_read + b * (2 * CH * 16);
+      // Fragments come from LDS RING at a time ahead of the matrix instruction that takes them (the scheduler is told so: left
+      // alone it reads each just before its use and waits).
+      constexpr int RING = DH == 256 ? 4 : 8;
+      constexpr int NK = NS * KS, NV = NS * 2 * DT;
+      auto k_at = [&](int i) {   // chunk k of sub-tile u
+        const int u = i / KS, k = i % KS;
+        return *reinterpret_cast<const u32x4*>(smem + (kl ^ ((k & 3) << 5)) + (k >> 2) * 128 + u * 32 * KC * 16);
+      };
+      auto v_at = [&](int i) {   // 16 keys ug, columns 32 d
+        const int ug = i / DT, d = i % DT;
+        return *reinterpret_cast<const u32x4*>(smem + (vl ^ (ug << 5)) + d * 32 * VC * 16);
+      };
       floatx16 s[NS];
+      u32x4 ring[RING];
+      __builtin_amdgcn_s_setprio(1);   // the SIMD's other wave, of another workgroup, has its softmax done meanwhile
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int u = 0; u < NS; ++u) {
+      for (int i = 0; i < RING; ++i) ring[i] = k_at(i);
+#pragma unroll
+      for (int u = 0; u < NS; ++u)
 #pragma unroll
         for (int e = 0; e < 16; ++e) s[u][e] = 0.0f;
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const u32x4 kf = *reinterpret_cast<const u32x4*>(smem + (kl ^ ((k & 3) << 5)) + (k >> 2) * 128 + u * 32 * KC * 16);
-          s[u] = Ty::mfma32(kf, qf[k], s[u]);
-        }
+      for (int i = 0; i < NK; ++i) {
+        s[i / KS] = Ty::mfma32(ring[i % RING], qf[i % KS], s[i / KS]);
+        if (i + RING < NK) ring[i % RING] = k_at(i + RING);
+        else if (i + RING - NK < RING) ring[i % RING] = v_at(i + RING - NK);   // V's first ones wait through the softmax
       }
+      __builtin_amdgcn_sched_group_barrier(0x100, RING, 0);   // LDS reads
+#pragma unroll
+      for (int i = 0; i < NK; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);    // a matrix instruction
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      }
+      __builtin_amdgcn_s_setprio(0);
       if (a.cap_out > 0.0f) {   // (uniform)
 #pragma unroll
         for (int u = 0; u < NS; ++u)
@@ -582,27 +626,39 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 4))
         ze = 1.0f;
         me = 0.0f;
       }
-      u32x4 pf[NS][2];
+      // probabilities of 16 keys, then their products, while the next 16 keys' probabilities are made
+      u32x4 pf[2];
+      auto exps = [&](int ug, u32x4& p) {
 #pragma unroll
-      for (int u = 0; u < NS; ++u)
-#pragma unroll
-        for (int g = 0; g < 2; ++g)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float x = __builtin_amdgcn_exp2f(fmaf(s[u][8 * g + 2 * j], ze, -me));
-            const float y = __builtin_amdgcn_exp2f(fmaf(s[u][8 * g + 2 * j + 1], ze, -me));
-            l += x + y;
-            pf[u][g][j] = Ty::round2(x, y);   // rounded to the cache's type: half a step of each probability
-          }
-      auto v_at = [&](int d, int u, int g) {
-        return *reinterpret_cast<const u32x4*>(smem + (vl ^ ((2 * u + g) << 5)) + d * 32 * VC * 16);
+        for (int j = 0; j < 4; ++j) {
+          const float x = __builtin_amdgcn_exp2f(fmaf(s[ug >> 1][8 * (ug & 1) + 2 * j], ze, -me));
+          const float y = __builtin_amdgcn_exp2f(fmaf(s[ug >> 1][8 * (ug & 1) + 2 * j + 1], ze, -me));
+          l += x + y;
+          p[j] = Ty::round2(x, y);   // rounded to the cache's type: half a step of each probability
+        }
       };
+      __builtin_amdgcn_sched_barrier(0);
+      exps(0, pf[0]);
 #pragma unroll
-      for (int u = 0; u < NS; ++u)
+      for (int ug = 0; ug < 2 * NS; ++ug) {
+        if (ug + 1 < 2 * NS) exps(ug + 1, pf[(ug + 1) & 1]);
 #pragma unroll
-        for (int g = 0; g < 2; ++g)
+        for (int d = 0; d < DT; ++d) {
+          const int i = ug * DT + d;
+          o[d] = Ty::mfma32(ring[(NK + i) % RING], pf[ug & 1], o[d]);
+          if (i + RING < NV) ring[(NK + i) % RING] = v_at(i + RING);
+        }
+      }
+      if constexpr (DH < 256) {   // (at 256 the registers leave the scheduler no choice)
+        constexpr int VALU = 8 * 4 / DT;   // about the vector instructions of 8 scores beside one of DT matrix instructions
+        __builtin_amdgcn_sched_group_barrier(0x402, 8 * 4, 0);
 #pragma unroll
-          for (int d = 0; d < DT; ++d) o[d] = Ty::mfma32(v_at(d, u, g), pf[u][g], o[d]);
+        for (int i = 0; i < NV; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+          if (i < NV - DT) __builtin_amdgcn_sched_group_barrier(0x402, VALU, 0);
+        }
+      }
     };
     const int t0 = lo / BK, t_end = (hi + BK - 1) / BK;
     // the window holds a tile's pages and the next one's
@@ -610,18 +666,20 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 4))
       if (!win.holds(entry(BK * t)) || !win.holds(entry(BK * (t + 2) - 1))) win.load(a, table, entry(BK * t));
     };
     win.load(a, table, entry(BK * t0));
-    copy(0, t0);
+    copy_k(0, t0);
+    copy_v(0, t0);
     for (int t = t0; t < t_end; ++t) {
       const int b = (t - t0) & 1;
       __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): this wave's copies of the tile have landed
       __syncthreads();                      // and everyone's; the other buffer has been read
       look(t);
-      if (t + 1 < t_end) copy(b ^ 1, t + 1);
+      if (t + 1 < t_end) {
+        copy_k(b ^ 1, t + 1);
+        copy_v(b ^ 1, t + 1);
+      }
       // The same for the whole workgroup: V of keys that are no one's becomes zero bits; so do infinities and NaN that not all
       // rows see, which are added to the rows that do at the end (wild)
-      bool ours = BK * t >= lo && BK * t + BK - 1 < hi;
-#pragma unroll
-      for (int i = 0; i < PG; ++i) ours = ours && win.at(entry(BK * t + 16 * i)) >= 0;
+      const bool ours = BK * t >= lo && BK * t + BK - 1 < hi && win.all(entry(BK * t), entry(BK * t + BK - 1));
       if (!ours || BK * t + BK - 1 > tile_a || (a.window > 0 && BK * t <= tile_b - a.window)) {
         bool found = false;
 #pragma unroll
@@ -697,19 +755,23 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a) {
   st.tile = row / a.rows;
   const RowTile r = row_tile(a, st);
   const int n = max(1, r.active);   // a tile without keys is written by split 0
-  const float2* ml = a.part_ml + th * a.splits;
-  float mm = kNegInf;
-  for (int s = 0; s < n; ++s) mm = fmaxf(mm, ml[s].x);
+  // a lane for each part's maximum and sum (at most 64 parts), then the parts in order
+  const float2 mine = lane < n ? a.part_ml[th * a.splits + lane] : make_float2(kNegInf, 0.0f);
+  float mm = mine.x;
+#pragma unroll
+  for (int i = 1; i < 64; i <<= 1) mm = fmaxf(mm, __shfl_xor(mm, i, 64));
   const float mu = mm == kNegInf ? 0.0f : mm;
-  float ll = 0.0f, v[C];
+  const float f = __builtin_amdgcn_exp2f(mine.x - mu);
+  float ll = f * mine.y, v[C];
+#pragma unroll
+  for (int i = 1; i < 64; i <<= 1) ll += __shfl_xor(ll, i, 64);
 #pragma unroll
   for (int c = 0; c < C; ++c) v[c] = 0.0f;
-  for (int s = 0; s < n; ++s) {
-    const float f = __builtin_amdgcn_exp2f(ml[s].x - mu);
-    ll += f * ml[s].y;
-    const float* po = a.part_o + (th * a.splits + s) * DH + lane * C;
+  const float* po = a.part_o + th * a.splits * DH + lane * C;
+  for (int s = 0; s < n; ++s) {   // (not unrolled: short code starts sooner, 3.9 against 6.2 us for 8 parts of 8 rows)
+    const float fs = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), s));
 #pragma unroll
-    for (int c = 0; c < C; ++c) v[c] += f * po[c];
+    for (int c = 0; c < C; ++c) v[c] += fs * po[s * DH + c];
   }
   const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
   uint16_t* op = a.out + th * DH + lane * C;
@@ -744,10 +806,17 @@ AttnPlan plan_attn(const rq_kv_cache* c, int tokens, int seqs, int heads, int ma
   p.slots = rows / p.rows + seqs;
   const int64_t each = (rows + seqs - 1) / seqs;   // rows of a sequence on average
   const int64_t wgs = std::min<int64_t>(seqs, tokens) * ((each + p.rows - 1) / p.rows) * c->kv_heads;
-  const int64_t want = p.rows == kRowsSmall ? 4 * kCUs : 2 * kCUs;   // workgroups
-  const int64_t blocks = (max_len + kSplitKeys - 1) / kSplitKeys;
-  // a split takes at least 256 keys, so that joining stays cheap beside it
-  p.splits = (int)std::max<int64_t>(1, std::min({want / wgs, (blocks + 1) / 2, (int64_t)64}));
+  const int64_t blocks = ((int64_t)max_len + kSplitKeys - 1) / kSplitKeys;
+  int64_t splits;
+  if (p.rows == kRowsSmall) {
+    // 4 workgroups a CU, down to one block a split (a tile for each wave); 8 where that leaves 1024 keys to each, so that
+    // sequences of different lengths even out (64 sequences of 2,900 to 8,192 keys: 306 -> 286 us; 16 of 3,000: 23 us, 26 us with 8)
+    splits = std::max(std::min<int64_t>(4 * kCUs / wgs, blocks), std::min<int64_t>(8 * kCUs / wgs, max_len / 1024));
+  } else {
+    // 2 workgroups a CU, of two blocks at least, so that joining stays cheap beside them
+    splits = std::min<int64_t>(2 * kCUs / wgs, (blocks + 1) / 2);
+  }
+  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(splits, 64));
   return p;
 }
 
