@@ -52,45 +52,43 @@ __device__ __forceinline__ uint32_t f32_to_half(float v, int dtype) {
   return dtype == RQ_BF16 ? f32_to_bf16(v) : __builtin_bit_cast(uint16_t, (_Float16)v);
 }
 
-// VEC values (8 or 1) as they lie in memory.
-template <int VEC, bool WIDE>
+// Eight values, or the first `count` of them, as they lie in memory: 16-byte accesses whatever their alignment (rows and halves of
+// odd sizes begin anywhere), value by value where fewer than eight are left.
+template <bool WIDE>
 struct Raw {
-  static constexpr int N = VEC == 1 ? 1 : WIDE ? 8 : 4;
+  typedef unsigned int word4 __attribute__((ext_vector_type(4), aligned(2)));
+  static constexpr int N = WIDE ? 8 : 4;
   uint32_t w[N];
   __device__ __forceinline__ void load(const void* p, int64_t i) {
-    if constexpr (VEC == 1) {
-      if constexpr (WIDE) w[0] = static_cast<const uint32_t*>(p)[i];
-      else w[0] = static_cast<const uint16_t*>(p)[i];
-    } else {
-      const u32x4* s = reinterpret_cast<const u32x4*>(static_cast<const unsigned char*>(p) + i * (WIDE ? 4 : 2));
+    const word4* s = reinterpret_cast<const word4*>(static_cast<const unsigned char*>(p) + i * (WIDE ? 4 : 2));
 #pragma unroll
-      for (int j = 0; j < N; j += 4) {
-        const u32x4 v = s[j / 4];
+    for (int j = 0; j < N; j += 4) {
+      const u32x4 v = s[j / 4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[j + e] = v[e];
-      }
+      for (int e = 0; e < 4; ++e) w[j + e] = v[e];
     }
   }
   __device__ __forceinline__ float get(int j, int dtype) const {
     if constexpr (WIDE) return __uint_as_float(w[j]);
-    if constexpr (VEC == 1) return half_to_f32(w[0], dtype);
     return half_to_f32((w[j / 2] >> (16 * (j & 1))) & 0xffffu, dtype);
   }
   __device__ __forceinline__ void set(int j, float v, int dtype) {   // in the order of j
     if constexpr (WIDE) w[j] = __float_as_uint(v);
-    else if constexpr (VEC == 1) w[0] = f32_to_half(v, dtype);
     else if (j & 1) w[j / 2] |= f32_to_half(v, dtype) << 16;
     else w[j / 2] = f32_to_half(v, dtype);
   }
   __device__ __forceinline__ void store(void* p, int64_t i) const {
-    if constexpr (VEC == 1) {
-      if constexpr (WIDE) static_cast<uint32_t*>(p)[i] = w[0];
-      else static_cast<uint16_t*>(p)[i] = (uint16_t)w[0];
-    } else {
-      u32x4* d = reinterpret_cast<u32x4*>(static_cast<unsigned char*>(p) + i * (WIDE ? 4 : 2));
+    word4* d = reinterpret_cast<word4*>(static_cast<unsigned char*>(p) + i * (WIDE ? 4 : 2));
 #pragma unroll
-      for (int j = 0; j < N; j += 4) d[j / 4] = u32x4{w[j], w[j + 1], w[j + 2], w[j + 3]};
-    }
+    for (int j = 0; j < N; j += 4) d[j / 4] = u32x4{w[j], w[j + 1], w[j + 2], w[j + 3]};
+  }
+  static __device__ __forceinline__ float load1(const void* p, int64_t i, int dtype) {
+    if constexpr (WIDE) return static_cast<const float*>(p)[i];
+    return half_to_f32(static_cast<const uint16_t*>(p)[i], dtype);
+  }
+  static __device__ __forceinline__ void store1(void* p, int64_t i, float v, int dtype) {
+    if constexpr (WIDE) static_cast<float*>(p)[i] = v;
+    else static_cast<uint16_t*>(p)[i] = (uint16_t)f32_to_half(v, dtype);
   }
 };
 
@@ -106,16 +104,26 @@ struct RopeTile {
   }
 };
 
+// Items of a head: runs of 8 values (the last of each kind may hold fewer). Half layout: 8 pairs, their first values and, half further,
+// their second ones; interleaved: 4 pairs; then the values that pass.
+struct HeadItems {
+  int turned, all;
+  __host__ __device__ HeadItems(int size, int half, bool interleaved) {
+    turned = ((interleaved ? 2 * half : half) + 7) / 8;
+    all = turned + (size - 2 * half + 7) / 8;
+  }
+};
+
 // q and k: heads [h0, h1) of tokens [ta, tb) of the tile (k's heads behind q's).
-template <int VEC, bool INTERLEAVED, bool IN32, bool OUT32>
+template <bool INTERLEAVED, bool IN32, bool OUT32>
 __device__ __forceinline__ void rotate_heads(const RopeArgs& a, const RopeTile& tile, bool append, int ta, int tb, int h0, int h1,
                                              float2* turn) {
-  constexpr int F = VEC == 1 ? 1 : INTERLEAVED ? VEC / 2 : VEC;   // angles of an item
-  constexpr int AHEAD = VEC == 1 ? 2 : 4;                          // heads whose loads are under way
-  constexpr bool TWO = VEC == 1 || !INTERLEAVED;                   // the pairs' second values are a run of their own
+  typedef Raw<IN32> In;
+  typedef Raw<OUT32> Out;
+  constexpr int F = INTERLEAVED ? 4 : 8;   // angles of an item
+  constexpr int AHEAD = 4;                 // heads whose loads are under way
   const int rot = 2 * a.half;
-  const int turned = INTERLEAVED ? (VEC == 1 ? a.half : rot / VEC) : a.half / VEC;   // rotated items of a head
-  const int per_head = turned + (a.size - rot) / VEC;                                // and those that pass
+  const HeadItems items(a.size, a.half, INTERLEAVED);
   const int tid = threadIdx.x, n = tb - ta;
   for (int i = tid; i < n * a.half; i += kRopeThreads) {
     const int t = i / a.half;
@@ -127,72 +135,101 @@ __device__ __forceinline__ void rotate_heads(const RopeArgs& a, const RopeTile& 
     turn[i] = make_float2(c * a.mscale, (a.inverse ? -s : s) * a.mscale);
   }
   __syncthreads();
-  // threads: items of a head, then tokens, then heads side by side
-  const int wide = min(per_head, kRopeThreads);
-  const int slots = kRopeThreads / wide, slot = tid / wide;
+  // threads: items of a head, then tokens, then heads side by side (head_size <= 512: at most 65 items)
+  const int slots = kRopeThreads / items.all, slot = tid / items.all, c = tid - slot * items.all;
   const int ts = min(n, slots), hs = slots / ts;
   if (slot >= ts * hs) return;
   const int first_head = h0 + slot / ts;
-  for (int c = tid - slot * wide; c < per_head; c += wide) {
-    const bool turns = c < turned;
-    // where the item's values lie in a head: one run of VEC, or two that are rot/2 apart
-    const int at = !turns ? rot + (c - turned) * VEC : INTERLEAVED && VEC == 1 ? 2 * c : c * VEC;
-    const int second = turns ? (INTERLEAVED ? (VEC == 1 ? 1 : 0) : a.half) : 0;   // distance of the second run (0: none)
-    for (int t = ta + slot % ts; t < tb; t += ts) {
-      const int token = tile.t0 + t;
-      float cs[F], sn[F];
-      if (turns) {
+  const bool turns = c < items.turned;
+  const int at = turns ? 8 * c : rot + 8 * (c - items.turned);                          // the item's first value in a head
+  const int count = min(8, (turns ? (INTERLEAVED ? rot : a.half) : a.size) - at);      // and how many
+  for (int t = ta + slot % ts; t < tb; t += ts) {
+    const int token = tile.t0 + t;
+    float cs[F], sn[F];
 #pragma unroll
-        for (int j = 0; j < F; ++j) {
-          const float2 v = turn[(t - ta) * a.half + (VEC == 1 ? c : c * F) + j];
-          cs[j] = v.x;
-          sn[j] = v.y;
-        }
-      }
-      int page = -1;
-      if (append) page = tile.page(a, tile.place0 + t);
-      const int64_t in_page = append ? ((tile.place0 + t) & ((1 << a.page_shift) - 1)) : 0;
+    for (int j = 0; j < F; ++j) {
+      // (past the last pair, and for values that pass: any angle, not used)
+      const float2 v = turn[(t - ta) * a.half + min((INTERLEAVED ? 4 : 8) * c + j, a.half - 1)];
+      cs[j] = v.x;
+      sn[j] = v.y;
+    }
+    int page = -1;
+    if (append) page = tile.page(a, tile.place0 + t);
+    const int64_t in_page = append ? ((tile.place0 + t) & ((1 << a.page_shift) - 1)) : 0;
+    auto source = [&](int g, const void*& src) {
+      const bool is_k = g >= a.heads;
+      src = is_k ? a.k : a.q;
+      return (int64_t)token * (is_k ? a.k_stride : a.q_stride) + (int64_t)(is_k ? g - a.heads : g) * a.size + at;
+    };
+    auto target = [&](int g, void*& dst) {
+      const bool is_k = g >= a.heads;
+      dst = is_k ? a.cache.k : a.out;
+      return at + (is_k ? ((((int64_t)page * a.kv_heads + (g - a.heads)) << a.page_shift) + in_page) * a.size
+                        : (int64_t)token * a.o_stride + (int64_t)g * a.size);
+    };
+    if (count == 8) {
+      const int second = turns && !INTERLEAVED ? a.half : 0;
       for (int h = first_head; h < h1; h += AHEAD * hs) {
-        Raw<VEC, IN32> x1[AHEAD], x2[AHEAD];
+        In x1[AHEAD], x2[AHEAD];
 #pragma unroll
         for (int u = 0; u < AHEAD; ++u) {
-          const int g = min(h + u * hs, h1 - 1);   // (behind the last: that one again, not stored)
-          const bool is_k = g >= a.heads;
-          const void* src = is_k ? a.k : a.q;
-          const int64_t from = (int64_t)token * (is_k ? a.k_stride : a.q_stride) + (int64_t)(is_k ? g - a.heads : g) * a.size + at;
+          const void* src;
+          const int64_t from = source(min(h + u * hs, h1 - 1), src);   // (behind the last: that one again, not stored)
           x1[u].load(src, from);
-          if constexpr (TWO) x2[u].load(src, from + second);
+          if constexpr (!INTERLEAVED) x2[u].load(src, from + second);
         }
 #pragma unroll
         for (int u = 0; u < AHEAD; ++u) {
           const int g = h + u * hs;
           if (g >= h1) break;
-          const bool is_k = g >= a.heads;
-          if (is_k && page < 0) continue;
-          void* dst = is_k ? a.cache.k : a.out;
-          const int64_t to = at + (is_k ? ((((int64_t)page * a.kv_heads + (g - a.heads)) << a.page_shift) + in_page) * a.size
-                                        : (int64_t)token * a.o_stride + (int64_t)g * a.size);
-          Raw<VEC, OUT32> y1, y2;
+          if (g >= a.heads && page < 0) continue;
+          void* dst;
+          const int64_t to = target(g, dst);
+          Out y1, y2;
           if (!turns) {
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) y1.set(j, x1[u].get(j, a.in_dtype), a.out_dtype);
-          } else if constexpr (INTERLEAVED && VEC > 1) {
+            for (int j = 0; j < 8; ++j) y1.set(j, x1[u].get(j, a.in_dtype), a.out_dtype);
+          } else if constexpr (INTERLEAVED) {
 #pragma unroll
-            for (int j = 0; j < VEC; j += 2) {
+            for (int j = 0; j < 8; j += 2) {
               const float p = x1[u].get(j, a.in_dtype), q = x1[u].get(j + 1, a.in_dtype);
               y1.set(j, p * cs[j / 2] - q * sn[j / 2], a.out_dtype);
               y1.set(j + 1, q * cs[j / 2] + p * sn[j / 2], a.out_dtype);
             }
           } else {
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
+            for (int j = 0; j < 8; ++j) {
               const float p = x1[u].get(j, a.in_dtype), q = x2[u].get(j, a.in_dtype);
-              y1.set(j, p * cs[j % F] - q * sn[j % F], a.out_dtype);
-              y2.set(j, q * cs[j % F] + p * sn[j % F], a.out_dtype);
+              y1.set(j, p * cs[j] - q * sn[j], a.out_dtype);
+              y2.set(j, q * cs[j] + p * sn[j], a.out_dtype);
             }
           }
           y1.store(dst, to);
           if (second) y2.store(dst, to + second);
+        }
+      }
+    } else {   // the short last item of its kind: pair by pair
+      for (int g = first_head; g < h1; g += hs) {
+        if (g >= a.heads && page < 0) continue;
+        const void* src;
+        void* dst;
+        const int64_t from = source(g, src), to = target(g, dst);
+        const int step = turns && INTERLEAVED ? 2 : 1, second = INTERLEAVED ? 1 : a.half;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (j * step >= count || j >= F) break;
+          const float p = In::load1(src, from + j * step, a.in_dtype);
+          if (turns) {
+            const float q = In::load1(src, from + j * step + second, a.in_dtype);
+            Out::store1(dst, to + j * step, p * cs[j] - q * sn[j], a.out_dtype);
+            Out::store1(dst, to + j * step + second, q * cs[j] + p * sn[j], a.out_dtype);
+          } else {
+            Out::store1(dst, to + j * step, p, a.out_dtype);
+          }
+        }
+        if constexpr (INTERLEAVED) {   // (values that pass are single: up to seven)
+          if (!turns)
+            for (int j = F; j < count; ++j) Out::store1(dst, to + j, In::load1(src, from + j, a.in_dtype), a.out_dtype);
         }
       }
     }
@@ -200,22 +237,20 @@ __device__ __forceinline__ void rotate_heads(const RopeArgs& a, const RopeTile& 
 }
 
 // v: columns [d0, d1) of the tile's tokens, through LDS 64 at a time where there are many tokens.
-template <bool VEC, bool IN32>
+template <bool IN32>
 __device__ __forceinline__ void transpose_columns(const RopeArgs& a, const RopeTile& tile, int d0, int d1, uint16_t (*lds)[kRopeTile + 8]) {
   const int tid = threadIdx.x;
   const int mask = (1 << a.page_shift) - 1;
   uint16_t* cache = static_cast<uint16_t*>(a.cache.v);
   auto value = [&](int t, int d) {
-    Raw<1, IN32> x;
-    x.load(a.v, (int64_t)(tile.t0 + t) * a.v_stride + d);
-    return (uint16_t)f32_to_half(x.get(0, a.in_dtype), a.out_dtype);
+    return (uint16_t)f32_to_half(Raw<IN32>::load1(a.v, (int64_t)(tile.t0 + t) * a.v_stride + d, a.in_dtype), a.out_dtype);
   };
   // where column d (of all kv heads) of a place's page begins, and the place in it
   auto spot = [&](int page, int d, int place) {
     const int h = d / a.size;
     return ((((int64_t)page * a.kv_heads + h) * a.size + (d - h * a.size)) << a.page_shift) + (place & mask);
   };
-  if (tile.n < 8 || !VEC) {
+  if (tile.n < 8) {
     for (int d = d0 + tid; d < d1; d += kRopeThreads)
       for (int t = 0; t < tile.n; ++t) {
         const int page = tile.page(a, tile.place0 + t);
@@ -225,15 +260,17 @@ __device__ __forceinline__ void transpose_columns(const RopeArgs& a, const RopeT
   }
   const int lead = tile.place0 & (kRopeTile - 1);   // the tile's first place among its 64
   for (int c0 = d0; c0 < d1; c0 += 64) {
-    const int cols = min(64, d1 - c0);               // a multiple of 8
+    const int cols = min(64, d1 - c0);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int t = tid / 8 + 32 * i, c = 8 * (tid % 8);   // token of the tile, its 8 columns
-      if (t < tile.n && c < cols) {
-        Raw<8, IN32> x;
+      if (t < tile.n && c + 8 <= cols) {
+        Raw<IN32> x;
         x.load(a.v, (int64_t)(tile.t0 + t) * a.v_stride + c0 + c);
 #pragma unroll
         for (int j = 0; j < 8; ++j) lds[c + j][lead + t] = (uint16_t)f32_to_half(x.get(j, a.in_dtype), a.out_dtype);
+      } else if (t < tile.n) {
+        for (int j = c; j < cols; ++j) lds[j][lead + t] = value(t, c0 + j);
       }
     }
     __syncthreads();
@@ -256,8 +293,7 @@ __device__ __forceinline__ void transpose_columns(const RopeArgs& a, const RopeT
   }
 }
 
-// VEC values a thread and access: 8 (16-byte accesses of 16-bit types) or 1.
-template <int VEC, bool INTERLEAVED, bool IN32, bool OUT32>
+template <bool INTERLEAVED, bool IN32, bool OUT32>
 __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a, int append) {
   __shared__ __align__(16) float2 lds[kTurns];   // angles, or v's columns
   RopeTile tile;
@@ -284,34 +320,27 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a, int appe
     const int all = a.heads + (append ? a.kv_heads : 0), each = (all + a.shares - 1) / a.shares;
     const int run = share / a.shares, h0 = (share - run * a.shares) * each, h1 = min(all, h0 + each);
     const int ta = run * a.run, tb = min(tile.n, ta + a.run);
-    if (h0 < h1 && ta < tb) rotate_heads<VEC, INTERLEAVED, IN32, OUT32>(a, tile, append, ta, tb, h0, h1, lds);
+    if (h0 < h1 && ta < tb) rotate_heads<INTERLEAVED, IN32, OUT32>(a, tile, append, ta, tb, h0, h1, lds);
   } else {
     const int all = a.kv_heads * a.size, each = ((all + a.v_shares - 1) / a.v_shares + 63) / 64 * 64;
     const int d0 = (share - a.runs * a.shares) * each, d1 = min(all, d0 + each);
-    if (d0 < d1) transpose_columns<VEC == 8, IN32>(a, tile, d0, d1, reinterpret_cast<uint16_t(*)[kRopeTile + 8]>(lds));
+    if (d0 < d1) transpose_columns<IN32>(a, tile, d0, d1, reinterpret_cast<uint16_t(*)[kRopeTile + 8]>(lds));
   }
 }
 
-bool aligned16(const void* p) { return (uintptr_t)p % 16 == 0; }
-
-template <int VEC, bool INTERLEAVED>
+template <bool INTERLEAVED>
 void launch_types(const RopeArgs& a, int append, dim3 grid, hipStream_t stream) {
   const dim3 block(kRopeThreads);
   if (a.in_dtype == RQ_F32) {
-    if (a.out_dtype == RQ_F32) hipLaunchKernelGGL((rope_kernel<VEC, INTERLEAVED, true, true>), grid, block, 0, stream, a, append);
-    else hipLaunchKernelGGL((rope_kernel<VEC, INTERLEAVED, true, false>), grid, block, 0, stream, a, append);
+    if (a.out_dtype == RQ_F32) hipLaunchKernelGGL((rope_kernel<INTERLEAVED, true, true>), grid, block, 0, stream, a, append);
+    else hipLaunchKernelGGL((rope_kernel<INTERLEAVED, true, false>), grid, block, 0, stream, a, append);
   } else {
-    if (a.out_dtype == RQ_F32) hipLaunchKernelGGL((rope_kernel<VEC, INTERLEAVED, false, true>), grid, block, 0, stream, a, append);
-    else hipLaunchKernelGGL((rope_kernel<VEC, INTERLEAVED, false, false>), grid, block, 0, stream, a, append);
+    if (a.out_dtype == RQ_F32) hipLaunchKernelGGL((rope_kernel<INTERLEAVED, false, true>), grid, block, 0, stream, a, append);
+    else hipLaunchKernelGGL((rope_kernel<INTERLEAVED, false, false>), grid, block, 0, stream, a, append);
   }
 }
 
 hipError_t launch(RopeArgs& a, bool interleaved, int append, int tiles, hipStream_t stream) {
-  const int ib = a.in_dtype == RQ_F32 ? 4 : 2, ob = a.out_dtype == RQ_F32 ? 4 : 2;
-  // 16-byte accesses where every row and every half begins at 16 bytes and holds whole 8s
-  bool vec = a.size % 8 == 0 && (interleaved ? 2 * a.half : a.half) % 8 == 0 && aligned16(a.q) && aligned16(a.out) &&
-             a.q_stride * ib % 16 == 0 && a.o_stride * ob % 16 == 0;
-  if (append) vec = vec && aligned16(a.k) && a.k_stride * ib % 16 == 0 && aligned16(a.v) && a.v_stride * ib % 16 == 0;
   // Workgroups of a tile. A thread that keeps its angles walks over at least four heads where there are tokens enough; about 8
   // workgroups a CU beyond that do not pay, since each computes its angles again. (append of 8,100 tokens x 40 heads x 128: 43 us with two
   // heads a share and v in one share, the figure below with these.)
@@ -319,19 +348,13 @@ hipError_t launch(RopeArgs& a, bool interleaved, int append, int tiles, hipStrea
   const int per_tile = std::min(kRopeTile, append ? std::max(1, a.tokens / std::max(1, a.batch.seqs)) : a.tokens);   // tokens
   a.run = std::min(16, kTurns / a.half);
   a.runs = (std::min(kRopeTile, append ? kRopeTile : a.tokens) + a.run - 1) / a.run;
-  const int per_head = (interleaved ? (vec ? 2 * a.half / 8 : a.half) : a.half / (vec ? 8 : 1)) + (a.size - 2 * a.half) / (vec ? 8 : 1);
-  const int side = std::max(1, kRopeThreads / std::max(1, std::min(per_head, kRopeThreads)) / std::min(per_tile, a.run));   // heads side by side
+  const int side = std::max(1, kRopeThreads / HeadItems(a.size, a.half, interleaved).all / std::min(per_tile, a.run));   // heads side by side
   const int busy = append ? std::min(tiles, a.tokens / kRopeTile + a.batch.seqs) : tiles;
   a.shares = std::max(1, std::min(all / (4 * side), 8 * kCUs / std::max(1, busy * ((per_tile + a.run - 1) / a.run))));
   a.v_shares = append ? std::max(1, std::min((a.kv_heads * a.size + 63) / 64, 8 * kCUs / std::max(1, busy))) : 0;
   const dim3 grid((unsigned)tiles, (unsigned)(a.runs * a.shares + a.v_shares));
-  if (interleaved) {
-    if (vec) launch_types<8, true>(a, append, grid, stream);
-    else launch_types<1, true>(a, append, grid, stream);
-  } else {
-    if (vec) launch_types<8, false>(a, append, grid, stream);
-    else launch_types<1, false>(a, append, grid, stream);
-  }
+  if (interleaved) launch_types<true>(a, append, grid, stream);
+  else launch_types<false>(a, append, grid, stream);
   return hipGetLastError();
 }
 
