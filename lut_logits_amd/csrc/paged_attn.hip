@@ -605,20 +605,22 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 4))
 #pragma unroll
         for (int e = 0; e < 16; e += 2) mt = fmaxf(fmaxf(mt, s[u][e]), s[u][e + 1]);
       mt = fmaxf(mt, __shfl_xor(mt, 32, 64));
+      // The reference that the exponentials are taken against follows the maximum only where it has grown by more than 8 (base 2):
+      // probabilities up to 2^8 cost no precision, and most tiles are spared the rescaling of o.
       const float mn = fmaxf(m, mt);
-      const float mu = mn == kNegInf ? 0.0f : mn * zs;
-      if (__any(mn > m)) {   // some row's maximum grew
+      if (__any((mn - m) * zs > 8.0f)) {
         const float f = __builtin_amdgcn_exp2f(mn == kNegInf ? 0.0f : (m - mn) * zs);
         l *= f;
 #pragma unroll
         for (int d = 0; d < DT; ++d) o[d] *= f;
         m = mn;
       }
+      const float mu = m == kNegInf ? 0.0f : m * zs;
       // One multiply-add a score. The rounding of mu is then a factor common to the row, 2^(|mu| 2^-24) at most; where that is more
       // than 2^-14, the differences are taken first.
       float ze = zs, me = mu;
       if (__any(fabsf(mu) > 1024.0f)) {
-        const float top = mn == kNegInf ? 0.0f : mn;
+        const float top = m == kNegInf ? 0.0f : m;
 #pragma unroll
         for (int u = 0; u < NS; ++u)
 #pragma unroll
