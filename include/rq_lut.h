@@ -458,8 +458,8 @@ typedef struct rq_kv_cache {
  * and where their caches lie. All arrays are device int32.
  *   seqs, tokens   number of sequences and rows of the packed tensors
  *   cu_q    [seqs + 1], rising: tokens cu_q[s] .. cu_q[s+1]-1 are sequence s's
- *           new ones (none is fine; rows from cu_q[seqs] on belong to no one and are
- *           left as they are)
+ *           new ones (none is fine; rows before cu_q[0] and from cu_q[seqs] on
+ *           belong to no one and are left as they are)
  *   lens    [seqs]: tokens of each sequence in the cache, the new ones among
  *           them as its last: new token i of n lies at place lens[s] - n + i
  *   table   [seqs][max_pages]: the page of places j*page_size .. of each sequence

@@ -78,7 +78,7 @@ __device__ __forceinline__ RowTile row_tile(const AttnArgs& a, const SeqTile& st
   r.n = st.n;
   r.place0 = st.len - st.n;
   r.row0 = st.tile * a.rows;
-  r.rows = min(a.rows, st.n * a.group - r.row0);
+  r.rows = st.tile < 0 ? 0 : min(a.rows, st.n * a.group - r.row0);   // (rows before the first sequence are no one's)
   if (r.rows <= 0) return r;
   const int first = r.place0 + r.row0 / a.group, last = r.place0 + (r.row0 + r.rows - 1) / a.group;
   const int capacity = (int)min((int64_t)a.batch.max_pages << a.page_shift, (int64_t)1 << 30);

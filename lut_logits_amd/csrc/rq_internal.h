@@ -87,7 +87,7 @@ __device__ __forceinline__ int floor_div(int a, int b) { return a >= 0 ? a / b :
 
 struct SeqTile {
   int seq;    // -1: none
-  int tile;   // the tile's number in the sequence (may lie behind its last)
+  int tile;   // the tile's number in the sequence (may lie behind its last, or before its first where cu_q[0] > 0)
   int t0, n;  // the sequence's first token and number of tokens
   int len;    // keys in the cache, the new ones among them
 };

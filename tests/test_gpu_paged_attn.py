@@ -218,6 +218,19 @@ def test_strided_queries_and_rows_behind():
         assert bool((out[n:] == 2.5).all()) and bool((ws[need:] == 3).all())
 
 
+@pytest.mark.parametrize("new,lens,lead", [([1, 2], [40, 300], 60), ([70, 130], [70, 900], 400), ([0, 40], [5, 2000], 130)])
+def test_rows_before_the_first_sequence(new, lens, lead):
+    """cu_q that begins behind row 0: the rows before belong to no sequence and are left as they are."""
+    c = Case(6, new, lens, 4, 2, 64, 16, "bf16")
+    q = torch.full((lead + c.b.tokens, 4, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    q[lead:] = dev(c.q, torch.bfloat16)
+    cu, kept, table = c.meta()
+    out, lse = torch.full_like(q, 7.0), torch.full((lead + c.b.tokens, 4), 7.0, device="cuda")
+    la.paged_attn(q, c.upload(), cu + lead, kept, table, out=out, lse=lse)
+    assert bool((out[:lead] == 7.0).all()) and bool((lse[:lead] == 7.0).all())
+    c.check(out[lead:], lse[lead:])
+
+
 def test_many_sequences():
     """More sequences than one step of the search looks at, some without new tokens."""
     rng = np.random.default_rng(8)
