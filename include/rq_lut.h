@@ -456,13 +456,14 @@ typedef struct rq_kv_cache {
 /*
  * The new tokens of a batch of sequences, packed one sequence behind the other,
  * and where their caches lie. All arrays are device int32.
- *   seqs, tokens   number of sequences and rows of the packed tensors
+ *   seqs, tokens   number of sequences (<= 2^22) and rows of the packed tensors
+ *           (<= 2^29, times heads < 2^31; rq_paged_attn: tokens * heads / 16 + seqs * kv_heads < 2^24)
  *   cu_q    [seqs + 1], rising: tokens cu_q[s] .. cu_q[s+1]-1 are sequence s's
  *           new ones (none is fine; rows before cu_q[0] and from cu_q[seqs] on
  *           belong to no one and are left as they are)
  *   lens    [seqs]: tokens of each sequence in the cache, the new ones among
  *           them as its last: new token i of n lies at place lens[s] - n + i
- *   table   [seqs][max_pages]: the page of places j*page_size .. of each sequence
+ *   table   [seqs][max_pages] (< 2^31 entries): the page of places j*page_size .. of each sequence
  * Values are not known to the host. A page id outside [0, pages), or a place
  * beyond the table, is never read or written: its keys are no one's, and the
  * token is not stored. Pages of different sequences may be shared for reading;

@@ -695,7 +695,7 @@ rq_status check_heads(int32_t heads, int32_t head_dim) {
 }
 
 rq_status check_tokens(int32_t tokens, int32_t heads) {
-  if (tokens < 0 || (int64_t)tokens * heads >= ((int64_t)1 << 31))
+  if (tokens < 0 || tokens > (1 << 29) || (int64_t)tokens * heads >= ((int64_t)1 << 31))
     return fail(RQ_ERR_SHAPE, "tokens=%d with %d heads out of range", tokens, heads);
   return RQ_OK;
 }
@@ -736,10 +736,11 @@ rq_status check_cache(const rq_kv_cache* c) {
 
 rq_status check_batch(const rq_seq_batch* b, int32_t heads) {
   if (!b) return fail(RQ_ERR_NULL, "batch descriptor is NULL");
-  if (b->seqs < 0 || b->seqs > (1 << 24)) return fail(RQ_ERR_SHAPE, "seqs=%d out of range", b->seqs);
+  if (b->seqs < 0 || b->seqs > (1 << 22)) return fail(RQ_ERR_SHAPE, "seqs=%d out of range", b->seqs);
   rq_status s = check_tokens(b->tokens, heads);
   if (s != RQ_OK) return s;
-  if (b->max_pages < 0) return fail(RQ_ERR_SHAPE, "max_pages=%d < 0", b->max_pages);
+  if (b->max_pages < 0 || (int64_t)b->seqs * b->max_pages >= ((int64_t)1 << 31))
+    return fail(RQ_ERR_SHAPE, "max_pages=%d of %d sequences out of range", b->max_pages, b->seqs);
   if (b->seqs == 0 || b->tokens == 0) return RQ_OK;
   if (!b->cu_q || !b->lens || (!b->table && b->max_pages > 0)) return fail(RQ_ERR_NULL, "batch: cu_q, lens or table is NULL");
   if (!aligned(b->cu_q, 4) || !aligned(b->lens, 4) || !aligned(b->table, 4))
@@ -758,8 +759,9 @@ rq_status check_attn_call(const rq_kv_cache* c, int32_t tokens, int32_t seqs, in
   if (heads % c->kv_heads) return fail(RQ_ERR_SHAPE, "heads=%d is no multiple of kv_heads=%d", heads, c->kv_heads);
   s = check_tokens(tokens, heads);
   if (s != RQ_OK) return s;
-  if (seqs < 0 || ((int64_t)tokens * heads / c->kv_heads + seqs) * c->kv_heads >= ((int64_t)1 << 31))
-    return fail(RQ_ERR_SHAPE, "seqs=%d out of range", seqs);
+  // a launch holds fewer than 2^32 threads: tiles of 16 rows at least, 256 threads each
+  if (seqs < 0 || ((int64_t)tokens * heads / c->kv_heads / 16 + seqs) * c->kv_heads >= ((int64_t)1 << 24))
+    return fail(RQ_ERR_SHAPE, "tokens=%d with %d heads in seqs=%d out of range", tokens, heads, seqs);
   if (max_len < 0) return fail(RQ_ERR_SHAPE, "max_len=%d < 0", max_len);
   return RQ_OK;
 }

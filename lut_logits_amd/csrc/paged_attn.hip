@@ -743,7 +743,8 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 4))
 
 // ---------------------------------------------------------------- joining the splits
 
-// One wave a (token, head): the parts in split order. Tokens of no sequence are left as they are.
+// One wave a (token, head): the parts in split order. Tokens of no sequence are left as they are. (Keys are split only where the
+// workgroups are few, so that the grid stays far below a launch's 2^32 threads.)
 template <int DH, bool F16>
 __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a) {
   constexpr int C = DH / 64;   // columns of a lane
@@ -881,7 +882,7 @@ hipError_t launch_paged_attn(const rq_seq_batch* batch, const rq_kv_cache* cache
   a.z_scale = scale * kLog2e;
   a.cap_in = softcap > 0.0f ? scale / softcap : 0.0f;
   a.cap_out = softcap > 0.0f ? softcap * kLog2e : 0.0f;
-  a.window = window;
+  a.window = std::min(window, 1 << 30);   // lengths end there
   a.splits = p.splits;
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;

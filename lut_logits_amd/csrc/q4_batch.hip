@@ -198,11 +198,11 @@ __global__ __launch_bounds__(256) void q4_cut_kernel(BatchArgs a, int nb, int gp
 }
 
 __global__ __launch_bounds__(256) void q4_add_kernel(const float* __restrict__ part, int ks, int64_t n, float* __restrict__ y) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= n) return;
-  float s = part[i];
-  for (int z = 1; z < ks; ++z) s += part[z * n + i];
-  y[i] = s;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    float s = part[i];
+    for (int z = 1; z < ks; ++z) s += part[z * n + i];
+    y[i] = s;
+  }
 }
 
 struct BatchPlan {
@@ -212,7 +212,7 @@ struct BatchPlan {
 };
 
 BatchPlan plan_batch(BatchArgs& a, int gpt) {
-  BatchPlan p;
+  BatchPlan p = {};   // T stays 0 where no plan fits a launch
   const int tiles = (a.B + 15) / 16, parts = q4_parts(a.src);
   p.NB = tiles <= 1 ? 1 : tiles == 2 ? 2 : 4;
   p.gy = (unsigned)((tiles + p.NB - 1) / p.NB);
@@ -226,6 +226,7 @@ BatchPlan plan_batch(BatchArgs& a, int gpt) {
       for (int ks = 1; ks <= (a.KT + wk - 1) / wk; ++ks) {
         const int kper = (a.KT + ks - 1) / ks, wr = kBatchWaves / wk;
         if ((a.KT + kper - 1) / kper != ks || (a.offsets && kper * gpt * p.NB > 1024)) continue;   // (64 KB of group sums)
+        if ((int64_t)(((a.RT + T - 1) / T + wr - 1) / wr) * ks * kBatchThreads >= (int64_t)1 << 32) continue;   // (threads of a launch)
         const double cus = std::ceil((double)(((a.RT + T - 1) / T + wr - 1) / wr) * p.gy * ks / kCUs);   // workgroups of a CU
         const double decode = T * 4 * (a.levels ? 96 : 56), product = T * 4 * 16.0 * parts * p.NB;
         const double simd = (kper + wk - 1) / wk * (std::max(decode, product) + 0.35 * std::min(decode, product)) * 2 * cus;
@@ -239,6 +240,7 @@ BatchPlan plan_batch(BatchArgs& a, int gpt) {
           a.kper = kper;
         }
       }
+  if (p.T == 0) return p;
   a.RG = (a.RT + p.T - 1) / p.T;
   const int wr = kBatchWaves / a.wk;
   p.gx = (unsigned)((((int64_t)a.RG + wr - 1) / wr) * a.ks);
@@ -294,6 +296,7 @@ hipError_t launch_q4_batch(Q4Args q, int gpt, void* ws, hipStream_t stream) {
   BatchArgs a = {};
   static_cast<Q4Args&>(a) = q;
   const BatchPlan p = plan_batch(a, gpt);
+  if (p.T == 0) return hipErrorInvalidConfiguration;
   char* w = static_cast<char*>(ws);
   a.xf = reinterpret_cast<u32x4*>(w);
   a.xsum = reinterpret_cast<float*>(w + p.xf);
@@ -309,7 +312,7 @@ hipError_t launch_q4_batch(Q4Args q, int gpt, void* ws, hipStream_t stream) {
   e = gpt == 4 ? launch_gpt<4>(a, p, stream) : gpt == 2 ? launch_gpt<2>(a, p, stream) : launch_gpt<1>(a, p, stream);
   if (e != hipSuccess || a.ks == 1) return e;
   const int64_t n = (int64_t)a.B * a.rows;
-  hipLaunchKernelGGL(q4_add_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream, a.part, a.ks, n, a.y);
+  hipLaunchKernelGGL(q4_add_kernel, dim3((unsigned)std::min<int64_t>((n + 255) / 256, 1 << 20)), dim3(256), 0, stream, a.part, a.ks, n, a.y);
   return hipGetLastError();
 }
 

@@ -193,37 +193,37 @@ __global__ __launch_bounds__(kFewThreads) __attribute__((amdgpu_waves_per_eu(4, 
 // One thread for the 8 codes of a word of the block layout; columns past D and rows past the matrix are code 0.
 __global__ void pack_q4_codes_kernel(const uint8_t* __restrict__ src, int64_t rows, int D, int KT, uint32_t* __restrict__ dst,
                                      int64_t words) {
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= words) return;
-  const int64_t blk = i >> 8;
-  const int in = (int)(i & 255), w = in & 3, i16 = (in >> 2) & 15, kg = in >> 6;
-  const int64_t r = (blk / KT) * 16 + i16;
-  const int k0 = (int)(blk % KT) * 128 + 32 * w + 8 * kg;
-  uint32_t out = 0;
-  if (r < rows) {
-    const int64_t row = r * ((D + 1) / 2);
-    for (int j = 0; j < 8; ++j) {
-      const int k = k0 + j;
-      if (k >= D) break;
-      const uint32_t byte = src[row + k / 2];
-      const uint32_t code = (k & 1) ? byte >> 4 : byte & 15u;
-      out |= code << (4 * (j < 4 ? 2 * j : 2 * (j - 4) + 1));
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < words; i += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t blk = i >> 8;
+    const int in = (int)(i & 255), w = in & 3, i16 = (in >> 2) & 15, kg = in >> 6;
+    const int64_t r = (blk / KT) * 16 + i16;
+    const int k0 = (int)(blk % KT) * 128 + 32 * w + 8 * kg;
+    uint32_t out = 0;
+    if (r < rows) {
+      const int64_t row = r * ((D + 1) / 2);
+      for (int j = 0; j < 8; ++j) {
+        const int k = k0 + j;
+        if (k >= D) break;
+        const uint32_t byte = src[row + k / 2];
+        const uint32_t code = (k & 1) ? byte >> 4 : byte & 15u;
+        out |= code << (4 * (j < 4 ? 2 * j : 2 * (j - 4) + 1));
+      }
     }
+    dst[i] = out;
   }
-  dst[i] = out;
 }
 
 template <typename E>
 __global__ void pack_q4_scales_kernel(const E* __restrict__ src, int64_t rows, int G, int KT, int gpt, E* __restrict__ dst,
                                       int64_t n) {
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= n) return;
-  const int g = (int)(i % gpt);
-  const int64_t row = i / gpt;   // block * 16 + row in it
-  const int64_t blk = row / 16;
-  const int64_t r = (blk / KT) * 16 + row % 16;
-  const int64_t group = (blk % KT) * gpt + g;
-  dst[i] = (r < rows && group < G) ? src[r * G + group] : (E)0;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
+    const int g = (int)(i % gpt);
+    const int64_t row = i / gpt;   // block * 16 + row in it
+    const int64_t blk = row / 16;
+    const int64_t r = (blk / KT) * 16 + row % 16;
+    const int64_t group = (blk % KT) * gpt + g;
+    dst[i] = (r < rows && group < G) ? src[r * G + group] : (E)0;
+  }
 }
 
 struct FewPlan {
@@ -305,9 +305,12 @@ static int64_t q4_blocks(int64_t rows, int D) { return ((rows + 15) / 16) * (int
 size_t q4_codes_bytes(int64_t rows, int D) { return (size_t)q4_blocks(rows, D) * 1024; }
 size_t q4_scale_count(int64_t rows, int D, int group) { return (size_t)q4_blocks(rows, D) * 16 * (128 / group); }
 
+// workgroups of 256 for n items, as many as one launch takes (the kernels go on from there)
+static unsigned pack_grid(int64_t n) { return (unsigned)std::min<int64_t>((n + 255) / 256, 1 << 20); }
+
 hipError_t launch_pack_q4_codes(const uint8_t* src, int64_t rows, int D, void* dst, hipStream_t stream) {
   const int64_t words = q4_blocks(rows, D) * 256;
-  hipLaunchKernelGGL(pack_q4_codes_kernel, dim3((unsigned)((words + 255) / 256)), dim3(256), 0, stream, src, rows, D,
+  hipLaunchKernelGGL(pack_q4_codes_kernel, dim3(pack_grid(words)), dim3(256), 0, stream, src, rows, D,
                      (D + 127) / 128, static_cast<uint32_t*>(dst), words);
   return hipGetLastError();
 }
@@ -316,7 +319,7 @@ hipError_t launch_pack_q4_scales(const void* src, int64_t rows, int D, int group
                                  hipStream_t stream) {
   const int64_t n = (int64_t)q4_scale_count(rows, D, group);
   const int G = (D + group - 1) / group, KT = (D + 127) / 128, gpt = 128 / group;
-  const dim3 grid((unsigned)((n + 255) / 256));
+  const dim3 grid(pack_grid(n));
   if (elem_bytes == 4)
     hipLaunchKernelGGL(pack_q4_scales_kernel<uint32_t>, grid, dim3(256), 0, stream, static_cast<const uint32_t*>(src), rows, G,
                        KT, gpt, static_cast<uint32_t*>(dst), n);

@@ -42,6 +42,13 @@ def test_q4_refusals(kw, status):
         assert B.lib().rq_last_error()
 
 
+def test_q4_more_than_a_launch():
+    """No split of 2^31 rows x 65536 columns with offsets fits one launch: an error and no launch."""
+    assert q4_call(rows=(1 << 31) - 1, D=65536, offsets=P, batch=64, group=32) == B.RQ_ERR_HIP
+    W = B.rq_q4_matrix((1 << 31) - 1, 65536, 32, B.RQ_BF16, P, P, P, None)
+    assert B.lib().rq_q4_matvec_workspace(ctypes.byref(W), B.RQ_F32, 0, 64) == 0
+
+
 def test_q4_sizes():
     lib = B.lib()
     assert lib.rq_q4_codes_bytes(17, 129) == 2 * 2 * 1024
@@ -68,7 +75,7 @@ def rope_call(x=P, x_dtype=B.RQ_F32, tokens=4, heads=2, size=64, xs=128, pos=P, 
 @pytest.mark.parametrize("kw,status", [
     (dict(heads=0), B.RQ_ERR_SHAPE), (dict(heads=4097), B.RQ_ERR_SHAPE), (dict(size=63), B.RQ_ERR_SHAPE),
     (dict(size=514), B.RQ_ERR_SHAPE), (dict(tokens=-1), B.RQ_ERR_SHAPE), (dict(tokens=1 << 30), B.RQ_ERR_SHAPE),
-    (dict(rot=0), B.RQ_ERR_SHAPE), (dict(rot=66), B.RQ_ERR_SHAPE), (dict(rot=3), B.RQ_ERR_SHAPE), (dict(xs=127), B.RQ_ERR_SHAPE),
+    (dict(tokens=(1 << 29) + 1, heads=1), B.RQ_ERR_SHAPE), (dict(rot=0), B.RQ_ERR_SHAPE), (dict(rot=66), B.RQ_ERR_SHAPE), (dict(rot=3), B.RQ_ERR_SHAPE), (dict(xs=127), B.RQ_ERR_SHAPE),
     (dict(os_=100), B.RQ_ERR_SHAPE), (dict(layout=2), B.RQ_ERR_DTYPE), (dict(x_dtype=3), B.RQ_ERR_DTYPE), (dict(out_dtype=-1), B.RQ_ERR_DTYPE),
     (dict(x=None), B.RQ_ERR_NULL), (dict(out=None), B.RQ_ERR_NULL), (dict(pos=None), B.RQ_ERR_NULL), (dict(freqs=None), B.RQ_ERR_NULL),
     (dict(x=P + 2), B.RQ_ERR_ALIGN), (dict(out=P + 2), B.RQ_ERR_ALIGN), (dict(freqs=P + 4), B.RQ_ERR_ALIGN), (dict(pos=P + 2), B.RQ_ERR_ALIGN),
@@ -95,7 +102,8 @@ SHARED = [
     (dict(page_size=512), B.RQ_ERR_SHAPE), (dict(kv_heads=0), B.RQ_ERR_SHAPE), (dict(kv_heads=257), B.RQ_ERR_SHAPE),
     (dict(head_dim=0), B.RQ_ERR_SHAPE), (dict(head_dim=65), B.RQ_ERR_SHAPE), (dict(dtype=B.RQ_F32), B.RQ_ERR_DTYPE),
     (dict(k=None), B.RQ_ERR_NULL), (dict(v=P + 8), B.RQ_ERR_ALIGN), (dict(seqs=-1), B.RQ_ERR_SHAPE), (dict(tokens=-1), B.RQ_ERR_SHAPE),
-    (dict(tokens=1 << 30), B.RQ_ERR_SHAPE), (dict(max_pages=-1), B.RQ_ERR_SHAPE), (dict(cu_q=None), B.RQ_ERR_NULL),
+    (dict(tokens=1 << 30), B.RQ_ERR_SHAPE), (dict(max_pages=-1), B.RQ_ERR_SHAPE),
+    (dict(seqs=(1 << 22) + 1), B.RQ_ERR_SHAPE), (dict(seqs=1 << 22, max_pages=512), B.RQ_ERR_SHAPE), (dict(cu_q=None), B.RQ_ERR_NULL),
     (dict(lens=None), B.RQ_ERR_NULL), (dict(table=None), B.RQ_ERR_NULL), (dict(lens=P + 2), B.RQ_ERR_ALIGN),
     (dict(heads=3), B.RQ_ERR_SHAPE), (dict(heads=0), B.RQ_ERR_SHAPE), (dict(q_stride=255), B.RQ_ERR_SHAPE), (dict(q=None), B.RQ_ERR_NULL),
     (dict(out=None), B.RQ_ERR_NULL), (dict(out=P), B.RQ_ERR_SHAPE), (dict(bad=P + 1), B.RQ_ERR_ALIGN),
@@ -122,6 +130,7 @@ def test_append_refusals(kw, status):
     (dict(head_dim=96, q_stride=384), B.RQ_ERR_SHAPE), (dict(window=-1), B.RQ_ERR_SHAPE), (dict(scale=0.0), B.RQ_ERR_SHAPE),
     (dict(scale=-0.125), B.RQ_ERR_SHAPE), (dict(scale=math.inf), B.RQ_ERR_SHAPE), (dict(scale=math.nan), B.RQ_ERR_SHAPE), (dict(max_len=-1), B.RQ_ERR_SHAPE),
     (dict(q_stride=260), B.RQ_ERR_ALIGN), (dict(q=P + 8), B.RQ_ERR_ALIGN), (dict(out=2 * P + 8), B.RQ_ERR_ALIGN), (dict(lse=P + 2), B.RQ_ERR_ALIGN),
+    (dict(tokens=1 << 26), B.RQ_ERR_SHAPE), (dict(seqs=1 << 20, kv_heads=16, heads=16, q_stride=1024, max_pages=1), B.RQ_ERR_SHAPE),
     (dict(ws=None), B.RQ_ERR_WORKSPACE), (dict(ws_bytes=16), B.RQ_ERR_WORKSPACE), (dict(ws=P + 16), B.RQ_ERR_ALIGN),
 ])
 def test_attn_refusals(kw, status):
