@@ -125,7 +125,6 @@ struct PageWindow {
   }
   __device__ __forceinline__ bool holds(int entry) const { return (unsigned)(entry - first) < 64u; }
   __device__ __forceinline__ int at(int entry) const { return __builtin_amdgcn_readlane(id, entry - first); }      // entry uniform
-  __device__ __forceinline__ int at_lane(int entry) const { return __shfl(id, entry - first, 64); }                // a lane's own
 };
 
 template <bool F16>
@@ -436,7 +435,8 @@ constexpr int tile_keys() { return DH == 256 ? 32 : 64; }
 // (4h .. 4h+3 and 8+4h .. 8+4h+3) are the eight consecutive keys 8h .. 8h+7.
 __device__ __forceinline__ int key_of_row(int i) { return (i & ~12) | ((i & 4) << 1) | ((i & 8) >> 1); }
 
-template <int DH, bool F16>
+// ONE: a tile of keys lies in one page.
+template <int DH, bool F16, bool ONE>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 4))) void attn_tile_kernel(AttnArgs a) {
   typedef Type<F16> Ty;
   constexpr int BK = tile_keys<DH>();
@@ -493,51 +493,68 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 4))
     const uint16_t* vbase = static_cast<const uint16_t*>(a.cache.v) + ((int64_t)kvh << a.page_shift) * DH;
     PageWindow win;
     auto entry = [&](int key) { return key >> a.page_shift; };
-    // Copies tile t into buffer b: 16 bytes a lane, lane after lane in LDS, so the swizzle is in what each lane fetches.
+    // Copies tile t into buffer b: 16 bytes a lane, lane after lane in LDS, so the swizzle is in what each lane fetches. Buffer loads:
+    // the base is the page's, the rest of the address does not change from tile to tile; and loads to LDS through global addresses
+    // would make the compiler wait for all of LDS's reads at each use of one (4000 tokens behind 4000 others, 32 heads of 128: 167 -> 147 us).
     // Chunk c = 256 j + tid of K is row c / KC: its 16 keys' page is the same for a whole wave, and what depends on the
-    // lane (its key among the 16, its place in the row) does not change with j. A lane's chunk of V keeps its keys
-    // over j, 8 of them, so one page.
+    // lane (its key among the 16, its place in the row) does not change with j.
     const int kx = tid / KC;                                    // row, less the part of j
-    const int k_lane = key_of_row(kx & 15) * DH + 8 * ((tid % KC) ^ (kx & 7));
-    const int vx = tid / VC;
-    const int v_keys = 8 * ((tid % VC) ^ (VC == 8 ? (vx & 7) : ((vx >> 1) & 3)));
+    const int k_lane = 2 * (key_of_row(kx & 15) * DH + 8 * ((tid % KC) ^ (kx & 7)));   // bytes, like all that follow
     constexpr int kRows = kThreads / KC;                        // K rows of 256 chunks: 8, 16 or 32
     // rows of chunk block j: their first key, less what the lane adds
     auto k_key = [&](int j) {
       return kRows == 8 ? 16 * (j >> 1) + 4 * (j & 1) : kRows * j + (kRows == 32 ? (wave * 8 & ~15) : 0);
     };
-    const bool one_page = BK <= 1 << a.page_shift;              // a tile lies in one page (uniform)
-    const int v_lane = (vx << a.page_shift) + v_keys;
-    auto put = [&](const uint16_t* src, unsigned char* dst) {
-      __builtin_amdgcn_global_load_lds((const void*)src, (lds_ptr_t)dst, 16, 0, 0);
+    // V in one page: chunk c is row c / VC, whose chunks are swizzled. In several: the 16 keys of a page's part lie together, [keys / 16]
+    // [DH][2 chunks], so that a wave's page is the same here too.
+    const int vx = ONE ? tid / VC : tid % (2 * DH) / 2;         // row, less the part of j
+    const int v_half = 8 * (ONE ? (tid % VC) ^ (VC == 8 ? (vx & 7) : ((vx >> 1) & 3)) : (tid & 1) ^ ((vx >> 2) & 1));   // keys before the lane's
+    const int v_lane = 2 * ((vx << a.page_shift) + v_half);
+    auto v_key = [&](int j) { return ONE ? 0 : (256 * j + 64 * wave) / (2 * DH) * 16; };            // first key of chunk block j
+    auto v_row = [&](int j) { return ONE ? kThreads / VC * j : 256 * j / 2 % DH / 128 * 128; };      // and its first row, beyond vx
+    const int page_bytes = 2 * DH << a.page_shift;              // of a kv head
+    auto rsrc = [&](const uint16_t* base, int key) {
+      return __builtin_amdgcn_make_buffer_rsrc((void*)(base + (int64_t)max(0, win.at(entry(key))) * page_elems), (short)0, page_bytes, 0x00020000);
+    };
+    auto put = [&](__amdgpu_buffer_rsrc_t from, int lane_at, int at, unsigned char* dst) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_ptr_t)dst, 16, lane_at, at, 0, 0);
     };
     constexpr int NC = CH / kThreads;                           // copies of a thread for K, and for V
     auto copy_k = [&](int b, int t) {
       unsigned char* dst = smem + (size_t)b * 2 * CH * 16 + wave * 1024;
-      if (one_page) {
-        const uint16_t* ks = kbase + (int64_t)max(0, win.at(entry(BK * t))) * page_elems + (int64_t)((BK * t) & pmask) * DH;
+      if constexpr (ONE) {
+        const __amdgpu_buffer_rsrc_t from = rsrc(kbase, BK * t);
+        const int first = ((BK * t) & pmask) * DH * 2;
 #pragma unroll
-        for (int j = 0; j < NC; ++j) put(ks + k_key(j) * DH + k_lane, dst + j * kThreads * 16);
+        for (int j = 0; j < NC; ++j) put(from, k_lane, first + k_key(j) * DH * 2, dst + j * kThreads * 16);
       } else {
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
           const int key = BK * t + (k_key(j) & ~15);
-          put(kbase + (int64_t)max(0, win.at(entry(key))) * page_elems + (int64_t)((key & pmask) + (k_key(j) & 15)) * DH + k_lane, dst + j * kThreads * 16);
+          put(rsrc(kbase, key), k_lane, ((key & pmask) + (k_key(j) & 15)) * DH * 2, dst + j * kThreads * 16);
         }
       }
     };
     auto copy_v = [&](int b, int t) {
       unsigned char* dst = smem + (size_t)b * 2 * CH * 16 + CH * 16 + wave * 1024;
-      const uint16_t* vs = one_page ? vbase + (int64_t)max(0, win.at(entry(BK * t))) * page_elems + ((BK * t) & pmask) + v_lane
-                                    : vbase + (int64_t)max(0, win.at_lane(entry(BK * t + v_keys))) * page_elems +
-                                          ((BK * t + v_keys) & pmask) + (vx << a.page_shift);
+      if constexpr (ONE) {
+        const __amdgpu_buffer_rsrc_t from = rsrc(vbase, BK * t);
+        const int first = ((BK * t) & pmask) * 2;
 #pragma unroll
-      for (int j = 0; j < NC; ++j) put(vs + ((kThreads / VC * j) << a.page_shift), dst + j * kThreads * 16);
+        for (int j = 0; j < NC; ++j) put(from, v_lane, first + (v_row(j) << a.page_shift) * 2, dst + j * kThreads * 16);
+      } else {
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+          const int key = BK * t + v_key(j);
+          put(rsrc(vbase, key), v_lane, (key & pmask) * 2 + (v_row(j) << a.page_shift) * 2, dst + j * kThreads * 16);
+        }
+      }
     };
-    // where this lane reads: chunk 2k + h of row i32 of K, chunk 4u + 2g + h of row i32 of V, both swizzled; the even parts of the
-    // chunk numbers are flipped in by the reader
+    // where this lane reads: chunk 2k + h of row i32 of K, chunk h of 16 keys of row i32 of V, both swizzled; what k, or the 16 keys, add
+    // is flipped in by the reader
     const uint32_t k_read = i32 * KC * 16 + ((h ^ (i32 & 7)) << 4);
-    const uint32_t v_read = CH * 16 + i32 * VC * 16 + ((h ^ (VC == 8 ? (i32 & 7) : ((i32 >> 1) & 3))) << 4);
+    const uint32_t v_read = CH * 16 + (ONE ? i32 * VC * 16 + ((h ^ (VC == 8 ? (i32 & 7) : ((i32 >> 1) & 3))) << 4)
+                                           : i32 * 32 + ((h ^ ((i32 >> 2) & 1)) << 4));
     const float zs = a.cap_out > 0.0f ? 1.0f : a.z_scale;   // scores enter the exponentials as zs * s - zs * max
     // One tile from buffer b. whole: every row of the wave sees every key
     auto attend = [&](int b, int t, bool whole) {
@@ -552,7 +569,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 4))
       };
       auto v_at = [&](int i) {   // 16 keys ug, columns 32 d
         const int ug = i / DT, d = i % DT;
-        return *reinterpret_cast<const u32x4*>(smem + (vl ^ (ug << 5)) + d * 32 * VC * 16);
+        return *reinterpret_cast<const u32x4*>(smem + (ONE ? (vl ^ (ug << 5)) + d * 32 * VC * 16 : vl + ug * DH * 32 + d * 1024));
       };
       floatx16 s[NS];
       u32x4 ring[RING];
@@ -688,10 +705,10 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 4))
         for (int j = 0; j < CH / kThreads; ++j) {
           u32x4* at = reinterpret_cast<u32x4*>(smem + b * (2 * CH * 16) + CH * 16 + (j * kThreads + tid) * 16);
           u32x4 v = *at;
-          const int pg = win.at_lane(entry(BK * t + v_keys));
+          const int pg = win.at(entry(BK * t + v_key(j)));
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int key = BK * t + v_keys + 2 * i;
+            const int key = BK * t + v_key(j) + v_half + 2 * i;
             v[i] &= (pg >= 0 && key >= lo && key < hi ? 0xffffu : 0u) | (pg >= 0 && key + 1 >= lo && key + 1 < hi ? 0xffff0000u : 0u);
             found |= not_finite<F16>(v[i]);
             v[i] = finite_halves<F16>(v[i]);
@@ -836,7 +853,8 @@ hipError_t launch_dh(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
     hipLaunchKernelGGL(kern, grid, dim3(kThreads), lds, stream, a);
   } else {
     const size_t lds = (size_t)4 * tile_keys<DH>() * DH * sizeof(uint16_t);
-    hipLaunchKernelGGL((attn_tile_kernel<DH, F16>), grid, dim3(kThreads), lds, stream, a);
+    if (a.cache.page_size >= tile_keys<DH>()) hipLaunchKernelGGL((attn_tile_kernel<DH, F16, true>), grid, dim3(kThreads), lds, stream, a);
+    else hipLaunchKernelGGL((attn_tile_kernel<DH, F16, false>), grid, dim3(kThreads), lds, stream, a);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
