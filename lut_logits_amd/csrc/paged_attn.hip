@@ -459,9 +459,13 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 4))
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int i32 = lane & 31, h = lane >> 5;
-  // last tiles first: under the causal mask they are the longest
-  const int slot = (int)blockIdx.x / a.cache.kv_heads, kvh = (int)blockIdx.x - slot * a.cache.kv_heads, split = blockIdx.y;
-  const SeqTile st = find_tile_rows(a.batch, a.rows, a.group, (int)gridDim.x / a.cache.kv_heads - 1 - slot);
+  // Last tiles first: under the causal mask they are the longest. Where two workgroups a CU hold them all, the CUs' second ones come
+  // shortest first, so that a long one meets a short one (1000 tokens behind 1000, 32 heads of 128: 41.4 -> 39.0 us).
+  const int kvh = (int)blockIdx.x % a.cache.kv_heads, parts = (int)gridDim.x / a.cache.kv_heads, first = kCUs / a.cache.kv_heads;
+  int part = (int)blockIdx.x / a.cache.kv_heads;
+  if (parts <= 2 * first && part >= first) part = parts - 1 - (part - first);
+  const int split = part % a.splits;
+  const SeqTile st = find_tile_rows(a.batch, a.rows, a.group, (parts - 1 - part) / a.splits);
   if (st.seq < 0) return;
   const RowTile r = row_tile(a, st);
   if (r.rows <= 0) return;
@@ -851,7 +855,7 @@ AttnPlan plan_attn(const rq_kv_cache* c, int tokens, int seqs, int heads, int ma
 
 template <int DH, bool F16>
 hipError_t launch_dh(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
-  const dim3 grid((unsigned)(p.slots * a.cache.kv_heads), (unsigned)p.splits);
+  const unsigned tiles = (unsigned)(p.slots * a.cache.kv_heads);
   if (p.rows == kRowsSmall) {
     const size_t lds = (size_t)4 * kRowsSmall * (DH + 4) * sizeof(float);
     auto kern = attn_rows_kernel<DH, F16>;
@@ -859,9 +863,10 @@ hipError_t launch_dh(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
       hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
       if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(kern, grid, dim3(kThreads), lds, stream, a);
+    hipLaunchKernelGGL(kern, dim3(tiles, (unsigned)p.splits), dim3(kThreads), lds, stream, a);
   } else {
     const size_t lds = (size_t)4 * tile_keys<DH>() * DH * sizeof(uint16_t);
+    const dim3 grid(tiles * p.splits);
     if (a.cache.page_size >= tile_keys<DH>()) hipLaunchKernelGGL((attn_tile_kernel<DH, F16, true>), grid, dim3(kThreads), lds, stream, a);
     else hipLaunchKernelGGL((attn_tile_kernel<DH, F16, false>), grid, dim3(kThreads), lds, stream, a);
   }
