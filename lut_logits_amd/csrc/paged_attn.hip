@@ -51,7 +51,7 @@ struct AttnArgs {
   int heads, group;            // query heads, and of one kv head
   int page_shift;
   int rows;                    // rows of a tile
-  float z_scale, cap_in, cap_out;   // base-2 scores: z * z_scale, or cap_out * tanh(z * cap_in)
+  float z_scale, cap_in, cap_out;   // base-2 scores: z * z_scale, or cap_out * (1 - 2 / (1 + 2^(z * cap_in)))
   int window;
   int splits;
   uint16_t* out;               // [tokens][heads][size]
@@ -165,8 +165,8 @@ struct Type<true> {
 // Base-2 score of a product q.k under a cap. tanh(u) = 1 - 2 / (1 + e^2u): its absolute error of 1e-7 is 1e-5 of a
 // probability at a cap of 50, far below the rounding of 16-bit outputs.
 __device__ __forceinline__ float capped(const AttnArgs& a, float z) {
-  const float e = __builtin_amdgcn_exp2f(z * a.cap_in * (2.0f * kLog2e));
-  return a.cap_out * (1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + e));
+  const float e = __builtin_amdgcn_exp2f(z * a.cap_in);
+  return fmaf(__builtin_amdgcn_rcpf(1.0f + e), -2.0f * a.cap_out, a.cap_out);
 }
 __device__ __forceinline__ float score(const AttnArgs& a, float z) {
   return a.cap_out > 0.0f ? capped(a, z) : z * a.z_scale;   // (uniform)
@@ -912,7 +912,7 @@ hipError_t launch_paged_attn(const rq_seq_batch* batch, const rq_kv_cache* cache
   a.page_shift = __builtin_ctz((unsigned)cache->page_size);
   a.rows = p.rows;
   a.z_scale = scale * kLog2e;
-  a.cap_in = softcap > 0.0f ? scale / softcap : 0.0f;
+  a.cap_in = softcap > 0.0f ? scale / softcap * (2.0f * kLog2e) : 0.0f;
   a.cap_out = softcap > 0.0f ? softcap * kLog2e : 0.0f;
   a.window = std::min(window, 1 << 30);   // lengths end there
   a.splits = p.splits;
