@@ -224,8 +224,11 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 8))
   constexpr int DT = DH / 16;   // column tiles of V
   __shared__ float2 ml[4][kRowsSmall];
   __shared__ int wilds[4];
-  extern __shared__ __align__(16) float osh[];   // [4][16][DH + 4]
+  extern __shared__ __align__(16) float osh[];   // [4][16][DH + 4], then q (QL)
   constexpr int OLD = DH + 4;
+  // At head size 256 the waves share q in LDS, [KS][64 lanes][16 bytes]: kept, it would take the registers of the loads under way (64 sequences
+  // of 8192 keys, 8 heads: 367 -> 286 us, 5.14 TB/s)
+  constexpr bool QL = DH == 256;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int i16 = lane & 15, kg = lane >> 4;
@@ -243,11 +246,16 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 8))
   const int tok = row / a.group;
   const int head = kvh * a.group + row - tok * a.group;
   const int place = r.place0 + tok;
-  u32x4 qf[KS];
+  u32x4 qf[QL ? 1 : KS];
+  u32x4* const q_lds = reinterpret_cast<u32x4*>(osh + 4 * kRowsSmall * OLD);
   {
     const uint16_t* qp = a.q + (int64_t)(r.t0 + tok) * a.q_stride + (int64_t)head * DH + 8 * kg;
 #pragma unroll
-    for (int s = 0; s < KS; ++s) qf[s] = *reinterpret_cast<const u32x4*>(qp + 32 * s);
+    for (int s = 0; s < KS; ++s) {
+      if constexpr (!QL) qf[s] = *reinterpret_cast<const u32x4*>(qp + 32 * s);
+      else if (s % 4 == wave) q_lds[64 * s + lane] = *reinterpret_cast<const u32x4*>(qp + 32 * s);   // (uniform)
+    }
+    if constexpr (QL) __syncthreads();
   }
   floatx4 o[DT];
 #pragma unroll
@@ -303,12 +311,14 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 8))
       if (t + 4 < t_end) pages(t + 4, n0, n1);
     }
     for (; t < t_end; t += 4) {
-      floatx4 s[2];
+      floatx4 s[2] = {floatx4{0.f, 0.f, 0.f, 0.f}, floatx4{0.f, 0.f, 0.f, 0.f}};
+      int at = lane;
+      if constexpr (QL) asm volatile("" : "+v"(at));   // read in every turn, not kept
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        s[u] = floatx4{0.f, 0.f, 0.f, 0.f};
+      for (int k = 0; k < KS; ++k) {
+        const u32x4 q = QL ? q_lds[64 * k + at] : qf[QL ? 0 : k];
 #pragma unroll
-        for (int k = 0; k < KS; ++k) s[u] = Ty::mfma16(kf[u][k], qf[k], s[u]);
+        for (int u = 0; u < 2; ++u) s[u] = Ty::mfma16(kf[u][k], q, s[u]);
       }
       const bool more = t + 4 < t_end;
       if (more) load_k(t + 4, n0, n1);
@@ -871,7 +881,7 @@ template <int DH, bool F16>
 hipError_t launch_dh(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
   const unsigned tiles = (unsigned)(p.slots * a.cache.kv_heads);
   if (p.rows == kRowsSmall) {
-    const size_t lds = (size_t)4 * kRowsSmall * (DH + 4) * sizeof(float);
+    const size_t lds = (size_t)4 * kRowsSmall * (DH + 4) * sizeof(float) + (DH == 256 ? DH / 32 * 1024 : 0);
     auto kern = attn_rows_kernel<DH, F16>;
     if (lds > 64 * 1024) {
       hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
