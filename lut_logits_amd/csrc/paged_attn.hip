@@ -797,13 +797,19 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 4))
 
 // ---------------------------------------------------------------- joining the splits
 
-// One wave a (token, head): the parts in split order. Tokens of no sequence are left as they are. (Keys are split only where the
-// workgroups are few, so that the grid stays far below a launch's 2^32 threads.)
-template <int DH, bool F16>
+// W waves a (token, head), each every W-th part, joined in wave order: four where there are few rows, whose time is the chain of loads
+// (one sequence of 8000 keys, 63 parts of 8 rows: the call 30.1 -> 15.7 us; 640 rows: 44.3 -> 41.7; but 1920 rows 22.8 -> 23.1, and 32000
+// rows of 2 parts 118 -> 151). A wave for four rows, their loads together, was no faster for many rows (6400 rows: 27.2 -> 30.5). Tokens of
+// no sequence are left as they are. (Keys are split only where the workgroups are few, so that the grid stays far below a launch's 2^32
+// threads.)
+constexpr int kJoinFew = 1024;
+template <int DH, bool F16, int W>
 __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a) {
   constexpr int C = DH / 64;   // columns of a lane
-  const int lane = threadIdx.x & 63;
-  const int64_t th = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
+  typedef float floats __attribute__((ext_vector_type(C)));
+  __shared__ floats sums[W > 1 ? W - 1 : 1][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t th = W > 1 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * (kThreads / 64) + wave;
   if (th >= (int64_t)a.batch.tokens * a.heads) return;
   const int t = (int)(th / a.heads);
   SeqTile st = find_token(a.batch, t);
@@ -819,16 +825,31 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a) {
   for (int i = 1; i < 64; i <<= 1) mm = fmaxf(mm, __shfl_xor(mm, i, 64));
   const float mu = mm == kNegInf ? 0.0f : mm;
   const float f = __builtin_amdgcn_exp2f(mine.x - mu);
-  float ll = f * mine.y, v[C];
+  float ll = f * mine.y;
 #pragma unroll
   for (int i = 1; i < 64; i <<= 1) ll += __shfl_xor(ll, i, 64);
+  floats v;
 #pragma unroll
   for (int c = 0; c < C; ++c) v[c] = 0.0f;
-  const float* po = a.part_o + th * a.splits * DH + lane * C;
-  for (int s = 0; s < n; ++s) {   // (not unrolled: short code starts sooner, 3.9 against 6.2 us for 8 parts of 8 rows)
-    const float fs = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), s));
+  const floats* po = reinterpret_cast<const floats*>(a.part_o + th * a.splits * DH) + lane;
+  auto weight = [&](int s) { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), s)); };
+  int s = W > 1 ? wave : 0;
+  if constexpr (W > 1) {
+    for (; s + 3 * W < n; s += 4 * W) {   // four parts' loads under way
+      floats x[4];
 #pragma unroll
-    for (int c = 0; c < C; ++c) v[c] += fs * po[s * DH + c];
+      for (int i = 0; i < 4; ++i) x[i] = po[(s + i * W) * 64];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v += weight(s + i * W) * x[i];
+    }
+  }
+  for (; s < n; s += W) v += weight(s) * po[s * 64];   // (not unrolled: short code starts sooner, 3.9 against 6.2 us for 8 parts of 8 rows)
+  if constexpr (W > 1) {
+    if (wave > 0) sums[wave - 1][lane] = v;
+    __syncthreads();
+    if (wave > 0) return;
+#pragma unroll
+    for (int w = 1; w < W; ++w) v += sums[w - 1][lane];
   }
   const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
   uint16_t* op = a.out + th * DH + lane * C;
@@ -899,8 +920,9 @@ hipError_t launch_dh(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
-  const int64_t n = ((int64_t)a.batch.tokens * a.heads + kThreads / 64 - 1) / (kThreads / 64);
-  hipLaunchKernelGGL((attn_join_kernel<DH, F16>), dim3((unsigned)n), dim3(kThreads), 0, stream, a);
+  const int64_t n = (int64_t)a.batch.tokens * a.heads;
+  if (n <= kJoinFew) hipLaunchKernelGGL((attn_join_kernel<DH, F16, 4>), dim3((unsigned)n), dim3(kThreads), 0, stream, a);
+  else hipLaunchKernelGGL((attn_join_kernel<DH, F16, 1>), dim3((unsigned)((n + kThreads / 64 - 1) / (kThreads / 64))), dim3(kThreads), 0, stream, a);
   return hipGetLastError();
 }
 
