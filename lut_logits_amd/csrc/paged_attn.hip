@@ -12,13 +12,19 @@
 // maxima and sums need one or two lane exchanges, and the rescaling factor is the lane's own. V is kept transposed in its
 // pages, so its operand is eight consecutive keys of a column: 16 bytes, as K's are.
 //
-// Two kernels by the rows a sequence brings (launch_paged_attn):
-// - rows_kernel, 16 rows (decode, drafts): HBM bound on the cache. Each of 4 waves takes every fourth tile of 32 keys straight from
+// Two kernels by the rows a sequence brings (plan_attn):
+// - attn_rows_kernel, 16 rows (decode, drafts): HBM bound on the cache. Each of 4 waves takes every fourth tile of 32 keys straight from
 //   memory into operand registers; the next tile's K is requested as soon as the current one's has been used, and V one step later.
 //   P is split in two parts of 16 bits: the matrix cores are idle anyway and the result is then exact to the output's rounding.
-// - tile_kernel, 128 rows (chunks, prompts): matrix-core bound. 4 waves of 32 rows share tiles of 64 keys (32 at head size 256)
-//   that go straight from memory to LDS, double buffered, one barrier a tile. P is rounded once to the cache's type.
-// Both split the keys over workgroups (the grid's second axis) when there are too few rows to fill the chip; the parts are joined by join_kernel
+//   64 sequences of 2,900 to 8,192 keys, 32 heads on 8 of 128, pages of 64: 287 us, 5.1 TB/s (a large copy: 5.07); 8 heads on 4 of
+//   256: 284 us, 5.2 TB/s. Few and short sequences are bound by their chain of loads: one of 1,000 keys 8 us and 3 us for joining.
+// - attn_tile_kernel, 128 rows (chunks, prompts): bound by the matrix cores beside the vector unit, which makes the probabilities
+//   (a tile of 64 keys at head size 128 is 32 matrix instructions, 1,024 clocks a wave, and about 200 vector ones). 4 waves of 32
+//   rows share tiles of 64 keys (32 at head size 256) that go straight from memory to LDS, double buffered, one barrier a tile; two
+//   workgroups a CU, so that one's matrix instructions meet the other's softmax. P is rounded once to the cache's type.
+//   4,000 tokens behind 4,000, 32 heads on 8 of 128: 146 us, 900 TFLOP/s; a prompt of 8,000, 16 heads on 4 of 256: 500 us, 1,045
+//   TFLOP/s (a large matrix product: 1,247); 256 tokens on 16,384 keys, 32 heads on 8: 87 us, 780 TFLOP/s, and 9 us for joining 4 parts.
+// Both split the keys over workgroups when there are too few rows to fill the chip; the parts are joined by attn_join_kernel
 // in a fixed order: no atomics, the same call gives the same bits.
 //
 // Keys that no row of a tile sees (places past the end, stale pages, before the window) are not multiplied: their V is set to zero
