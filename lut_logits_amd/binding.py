@@ -620,6 +620,17 @@ def _scratch(ws, need, dev):
     return torch.empty(need, dtype=torch.uint8, device=dev) if need else None
 
 
+_SIZES_KEPT = 4096
+
+
+def _keep(sizes, key, need):
+    """Keeps a call's workspace size with its handle: a bounded number of them, since lengths and batches change without end."""
+    if len(sizes) >= _SIZES_KEPT:
+        sizes.clear()
+    sizes[key] = need
+    return need
+
+
 class Q4Matrix:
     """A matrix [rows][D] in 4 bits with scales (and offsets) per group of columns, in the library's block layout
     (rq_q4_matrix in include/rq_lut.h; made by pack_q4, or from tensors that already hold the layout).
@@ -708,7 +719,7 @@ def q4_matvec(W, x, x2=None, prologue=RQ_PRO_NONE, ws=None, out=None):
         _arg(out, "out", torch.float32, numel=B * W.rows)
     need = W._ws.get((B, xt, prologue))
     if need is None:
-        need = W._ws[B, xt, prologue] = q4_matvec_workspace(W, B, x.dtype, prologue)
+        need = _keep(W._ws, (B, xt, prologue), q4_matvec_workspace(W, B, x.dtype, prologue))
     if need or ws is not None:
         ws = _scratch(ws, need, x.device)
     dev = _same_device("codes x x2 out ws", W.codes, x, x2, out, ws)
@@ -829,7 +840,7 @@ def paged_attn(q, cache, cu_q, lens, table, scale=None, softcap=0.0, window=0, m
         _arg(bad_pages, "bad_pages", torch.int32, min_numel=1)
     need = cache._ws.get((T, batch.seqs, heads, max_len))
     if need is None:
-        need = cache._ws[T, batch.seqs, heads, max_len] = paged_attn_workspace(cache, T, batch.seqs, heads, max_len)
+        need = _keep(cache._ws, (T, batch.seqs, heads, max_len), paged_attn_workspace(cache, T, batch.seqs, heads, max_len))
     if need or ws is not None:
         ws = _scratch(ws, need, q.device)
     dev = _same_device("cache q out cu_q lens table lse bad_pages ws", cache.k, q, out, cu_q, lens, table, lse, bad_pages, ws)

@@ -216,6 +216,13 @@ def test_binding_refusals():
     raises(lambda: la.paged_attn(q, cache, cu, lens, table), "GPU")
 
 
+def test_sizes_kept_are_bounded():
+    """A server's batches and lengths change without end: what a handle keeps of them does not grow with them."""
+    kept = {}
+    for i in range(3 * B._SIZES_KEPT):
+        assert B._keep(kept, (i, 1, 4, 2 * i), i) == i and len(kept) <= B._SIZES_KEPT
+
+
 def test_rope_freqs():
     f, m = la.rope_freqs(8, base=100.0, device="cpu")
     assert m == 1.0 and np.allclose(f.numpy(), [1, 100 ** -0.25, 0.1, 100 ** -0.75], rtol=1e-15)
