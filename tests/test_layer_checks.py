@@ -129,15 +129,16 @@ def test_append_refusals(kw, status):
 @pytest.mark.parametrize("kw,status", SHARED + [
     (dict(head_dim=96, q_stride=384), B.RQ_ERR_SHAPE), (dict(window=-1), B.RQ_ERR_SHAPE), (dict(scale=0.0), B.RQ_ERR_SHAPE),
     (dict(scale=-0.125), B.RQ_ERR_SHAPE), (dict(scale=math.inf), B.RQ_ERR_SHAPE), (dict(scale=math.nan), B.RQ_ERR_SHAPE), (dict(max_len=-1), B.RQ_ERR_SHAPE),
+    (dict(softcap=math.inf), B.RQ_ERR_SHAPE), (dict(softcap=math.nan), B.RQ_ERR_SHAPE), (dict(softcap=1e-39), B.RQ_ERR_SHAPE),
     (dict(q_stride=260), B.RQ_ERR_ALIGN), (dict(q=P + 8), B.RQ_ERR_ALIGN), (dict(out=2 * P + 8), B.RQ_ERR_ALIGN), (dict(lse=P + 2), B.RQ_ERR_ALIGN),
     (dict(tokens=1 << 26), B.RQ_ERR_SHAPE), (dict(seqs=1 << 20, kv_heads=16, heads=16, q_stride=1024, max_pages=1), B.RQ_ERR_SHAPE),
     (dict(ws=None), B.RQ_ERR_WORKSPACE), (dict(ws_bytes=16), B.RQ_ERR_WORKSPACE), (dict(ws=P + 16), B.RQ_ERR_ALIGN),
 ])
 def test_attn_refusals(kw, status):
     c, b, kw = split_kw(kw)
-    a = dict(q=P, q_stride=256, heads=4, scale=0.125, window=0, max_len=0, out=2 * P, lse=None, bad=None, ws=4 * P, ws_bytes=1 << 40)
+    a = dict(q=P, q_stride=256, heads=4, scale=0.125, softcap=0.0, window=0, max_len=0, out=2 * P, lse=None, bad=None, ws=4 * P, ws_bytes=1 << 40)
     a.update(kw)
-    assert B.lib().rq_paged_attn(ctypes.byref(b), ctypes.byref(c), a["q"], a["q_stride"], a["heads"], a["scale"], 0.0, a["window"], a["max_len"],
+    assert B.lib().rq_paged_attn(ctypes.byref(b), ctypes.byref(c), a["q"], a["q_stride"], a["heads"], a["scale"], a["softcap"], a["window"], a["max_len"],
                                  a["out"], a["lse"], a["bad"], a["ws"], a["ws_bytes"], None) == status
 
 
