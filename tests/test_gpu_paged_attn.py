@@ -95,6 +95,14 @@ def test_against_definition(new, lens, heads, kv, size, page, dtype, softcap, wi
     assert torch.equal(out, c.run(softcap=softcap, window=window))
 
 
+@pytest.mark.parametrize("new,size,page,window", [(1, 64, 16, 0), (1, 256, 16, 0), (3, 128, 16, 1500), (70, 64, 16, 0), (70, 128, 32, 0),
+                                                  (70, 256, 16, 0), (70, 256, 32, 1200), (70, 128, 16, 1500)])
+def test_long_tables(new, size, page, window):
+    """More table entries than are looked up at once (64), on both kernels, whatever the page."""
+    c = Case(new + size, [new, new], [2100, 2500], 4, 2, size, page, "bf16")
+    c.check(c.run(window=window), None, 0.0, window, one_rounding=new > 8)
+
+
 def test_max_len_exceeded():
     """A bound that is too low changes the split alone."""
     c = Case(1, [1, 40], [900, 1000], 2, 1, 64, 16, "bf16")
