@@ -168,7 +168,7 @@ __global__ __launch_bounds__(256) void q4_cut_kernel(BatchArgs a, int nb, int gp
   const int tile = blk / a.KT;
   const int b = (tile * nb + n) * 16 + i16, k0 = (blk - tile * a.KT) * 128 + 32 * step + 8 * kg;
   Q4Acts<SRC, 8> w;
-  w.load(a, min(b, a.B - 1), k0);
+  w.load_wide(a, min(b, a.B - 1), k0);
   float v[8], s = 0.0f;
   w.values(a, k0, v);
 #pragma unroll

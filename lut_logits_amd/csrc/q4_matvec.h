@@ -119,6 +119,32 @@ struct Q4Acts {
       if constexpr (SRC == kQ4Gelu) x2[j] = reinterpret_cast<const uint32_t*>(a.x2)[i];
     }
   }
+  // The same by 16 bytes at a time, whatever their alignment, where all N are there.
+  __device__ __forceinline__ void load_wide(const Q4Args& a, int b, int k) {
+    typedef unsigned int word4 __attribute__((ext_vector_type(4), aligned(2)));
+    if (k + N > a.D) return load(a, b, k);
+    const int64_t i = (int64_t)b * a.D + k;
+    if constexpr (SRC == kQ4F32 || SRC == kQ4Gelu) {
+#pragma unroll
+      for (int j = 0; j < N; j += 4) {
+        const u32x4 w = *reinterpret_cast<const word4*>(static_cast<const uint32_t*>(a.x) + i + j);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[j + e] = w[e];
+        if constexpr (SRC == kQ4Gelu) {
+          const u32x4 w2 = *reinterpret_cast<const word4*>(a.x2 + i + j);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x2[j + e] = w2[e];
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; j += 8) {
+        const u32x4 w = *reinterpret_cast<const word4*>(static_cast<const uint16_t*>(a.x) + i + j);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[j + e] = (w[e / 2] >> (16 * (e & 1))) & 0xffffu;
+      }
+    }
+  }
   __device__ __forceinline__ void values(const Q4Args& a, int k, float (&v)[N]) const {
 #pragma unroll
     for (int j = 0; j < N; ++j) {
