@@ -77,6 +77,20 @@ def test_in_place_and_strided():
     assert torch.equal(stacked[:, :64], before[:, :64]) and torch.equal(stacked[:, 64 + 256:], before[:, 64 + 256:])
 
 
+@pytest.mark.parametrize("size,rot,layout", [(254, 254, "half"), (250, 100, "interleaved"), (66, 22, "half"), (20, 20, "interleaved")])
+def test_sizes_of_no_whole_eights(size, rot, layout):
+    """Out of place the last items of a head overlap the ones before, in place they do not: the same bits."""
+    rng = np.random.default_rng(size)
+    x = ref.round_to(rng.standard_normal((70, 5, size)), "bf16")
+    pos = rng.integers(0, 5000, 70).astype(np.int32)
+    freqs, _ = la.rope_freqs(rot, device="cpu")
+    t = dev(x, torch.bfloat16)
+    y = la.rope(t, dev(pos), freqs.cuda(), layout)
+    check(host(y.float()), x, pos, freqs.numpy(), 1.0, layout, "bf16")
+    assert la.rope(t, dev(pos), freqs.cuda(), layout, out=t) is t
+    assert torch.equal(t, y)
+
+
 def test_gradient():
     """inverse=True is the gradient: <rope(x), g> = <x, rope^-1(g)>, against differences of the formula in 64 bits too."""
     rng = np.random.default_rng(4)
